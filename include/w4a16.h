@@ -100,8 +100,13 @@ enum {
     W4_ERR_WORKSPACE = 10, /* workspace NULL or smaller than w4a16_gemm_workspace_size  */
     W4_ERR_GIDX = 11,      /* (written to *status_out by the device) g_idx irregular    */
     W4_ERR_TIMEOUT = 12,   /* (device status word) a kernel gave up on a pipeline wait  */
-    W4_ERR_EXPERT_ROWS = 13 /* (device status word) w4a16_moe_gemm: an expert's row range
+    W4_ERR_EXPERT_ROWS = 13, /* (device status word) w4a16_moe_gemm: an expert's row range
                               was invalid or longer than max_rows_per_expert          */
+    W4_ERR_PAGE = 14,      /* (device) w4_kv8_*: a page number, length or offset read on
+                              the device was out of range                             */
+    W4_ERR_NO_PAGES = 15,  /* (device) w4_kv8_reserve / _fork: too few free pages       */
+    W4_ERR_SEQ = 16        /* (device) w4_kv8_*: a sequence number was out of range, or a
+                              fork's target was not empty or listed twice             */
 };
 
 enum { W4_F16 = 0, W4_BF16 = 1 };
@@ -385,6 +390,154 @@ W4_API w4_status w4_device_status(int32_t* status_out, int clear);
 W4_API w4_status w4_dequant(const int32_t* qw, const void* scales, const int32_t* zeros,
                      int K, int N, int group, int dtype, int layout, int out_f32,
                      void* w_out, void* stream);
+
+/*
+ * ---- 8-bit key-value cache --------------------------------------------------
+ *
+ * One layer's cache holds keys and values as float8_e4m3fn codes in pages of
+ * `page_size` tokens, [num_pages][kv_heads][page_size][head_dim], with one fp32
+ * scale for each page and head ([num_pages][kv_heads], keys and values apart):
+ *     value = code * scale.
+ * Sequence b's token j lives in page table[b][j / page_size], slot
+ * j % page_size. The calls below write it (w4_kv8_append), attend over it
+ * (w4_kv8_attention) and manage its pages. What they read on the device (page
+ * numbers, lengths, offsets) is checked there: a bad value is skipped, never
+ * followed, and W4_ERR_PAGE is recorded in the device status word.
+ *
+ * The descriptor is a HOST struct, read during the call.
+ *   The int32 arrays of these calls need 4-byte alignment only, so they may be
+ *   slices of larger ones.
+ *   head_dim 64 or 128; page_size 16, 32, 64 or 128; kv_heads 1..1024;
+ *   num_pages * kv_heads * page_size < 2^31 (else W4_ERR_SHAPE).
+ */
+typedef struct w4_kv8_cache {
+    void* k;        /* [num_pages][kv_heads][page_size][head_dim] e4m3 */
+    void* v;        /* the same                                       */
+    float* k_scale; /* [num_pages][kv_heads], finite and > 0          */
+    float* v_scale; /* the same                                       */
+    int num_pages, page_size, kv_heads, head_dim;
+} w4_kv8_cache;
+
+/* The queries of an attention call (a HOST struct, read during the call). */
+typedef struct w4_kv8_heads {
+    int q_heads; /* a multiple of kv_heads, at most 1024 */
+    int causal;  /* 0 or 1                               */
+    float scale; /* applied to q . k; finite             */
+} w4_kv8_heads;
+
+/*
+ * Quantise new keys and values into the cache. The batch's new tokens are
+ * packed: sequence b's are rows cu_q[b] .. cu_q[b+1]-1 of k_new and v_new, and
+ * become its tokens kv_lens[b] - n .. kv_lens[b] - 1 (n of them: kv_lens counts
+ * them already). For every page they touch and every head, keys and values
+ * apart:
+ *   fit  = the smallest power of two, 2^-40 at least, in which the page's new
+ *          elements stay within e4m3's 448 (infinities and NaN not counted);
+ *   s'   = max(fit, s) where the page held tokens of this sequence before, fit
+ *          where it did not;
+ *   the new codes are e4m3(x / s'), rounded to nearest even and saturated at
+ *   448 (NaN stays NaN), and the codes that were there become
+ *   e4m3(code * (s / s')) where s' > s. With power-of-two scales that changes
+ *   only the exponent, and rounds only what falls below e4m3's normal range.
+ * The result does not depend on how a sequence's tokens are cut into calls
+ * except through those roundings. A page that gets tokens belongs to one
+ * sequence (w4_kv8_fork gives every child a partial page of its own).
+ *   k_new, v_new  [total_q][kv_heads][head_dim] in dtype; a token's rows are
+ *            k_stride / v_stride elements apart (multiples of 8, at least
+ *            kv_heads * head_dim), so they may be slices of one projection.
+ *   table    [batch][table_stride] int32; kv_lens [batch]; cu_q [batch + 1],
+ *            non-decreasing from 0; max_q_len: at least every sequence's n.
+ * A sequence whose n exceeds max_q_len or kv_lens[b], or whose length does not
+ * fit the table, is left out (W4_ERR_PAGE). total_q == 0 or batch == 0: no-op.
+ */
+W4_API w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_stride,
+                               size_t v_stride, const w4_kv8_cache* cache,
+                               const int32_t* table, int table_stride, const int32_t* kv_lens,
+                               const int32_t* cu_q, int batch, int total_q, int max_q_len,
+                               int dtype, void* stream);
+
+/*
+ * Attention of new tokens over their sequences' cached keys and values:
+ *   out[i][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[i][h] . k_j),
+ * over the tokens j < kv_lens[b] of i's sequence b, head h reading kv head
+ * h / (q_heads / kv_heads). With causal != 0 the sequence's n queries are its
+ * last n tokens: query i sees j <= kv_lens[b] - n + i. With causal == 0 every
+ * query sees all kv_lens[b] tokens (attention to an encoder's states). A query
+ * that sees nothing gives 0. A NaN among a token's codes reaches the queries that
+ * see the token, and no other. Slots that hold no token of the sequence are never
+ * part of a result, whatever they contain.
+ *   q        [total_q][q_heads][head_dim] in dtype, a token's rows q_stride
+ *            elements apart (a multiple of 8, at least q_heads * head_dim).
+ *   out      [total_q][q_heads][head_dim] in dtype, contiguous; overlaps no input.
+ *            Rows at or past cu_q[batch] are not written.
+ *   table, kv_lens, cu_q, max_q_len as for w4_kv8_append; max_kv_len: at least
+ *            every kv_lens[b]. A sequence beyond either bound or its table row
+ *            gets zeros (W4_ERR_PAGE); a page number out of range counts as a
+ *            page without tokens (W4_ERR_PAGE).
+ *   workspace: at least w4_kv8_attention_workspace_size(...) bytes (may be NULL
+ *            when that is 0), no initialisation needed; else W4_ERR_WORKSPACE.
+ * q is taken in fp16 after a power-of-two scaling of each row (exact but for
+ * elements below 2^-28 of the row's largest), codes enter the products exactly, p is rounded to
+ * fp16, and scores, maxima, sums and products accumulate in fp32. Deterministic.
+ */
+W4_API size_t w4_kv8_attention_workspace_size(int batch, int total_q, int max_q_len,
+                                              int max_kv_len, int q_heads, int kv_heads,
+                                              int head_dim);
+W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_cache* cache,
+                                  const int32_t* table, int table_stride,
+                                  const int32_t* kv_lens, const int32_t* cu_q, void* out,
+                                  int batch, int total_q, int max_q_len, int max_kv_len,
+                                  const w4_kv8_heads* heads, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a pool are counted by refs [num_pages] int32 (0: free), and its
+ * sequences described by table [num_seqs][table_stride] and lens [num_seqs]
+ * (tokens held; 0: an empty slot). Table entries past a sequence's pages are -1.
+ * All four are device arrays that these calls change in place; every layer's
+ * cache uses the same page numbers. Each call is all or nothing: on an error it
+ * changes nothing. *status_out (device int32) receives W4_OK or the error, in
+ * stream order; with status_out NULL an error goes to the device status word.
+ * Results depend on the inputs alone: pages are handed out in ascending order.
+ * `workspace`: w4_kv8_pages_workspace_size(num_pages, n) bytes, n the number of
+ * sequences or pairs given (num_seqs for reserve and compact).
+ *
+ * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0) for every sequence, and
+ *     gives it the pages that takes: the lowest free ones, sequence by sequence.
+ * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
+ *     of src[i]. Full pages are shared (refs + 1); a last partial page is copied
+ *     into the next free page, which copy_src[i] -> copy_dst[i] says (-1, -1
+ *     where there is none): run w4_kv8_copy_pages on every layer with them.
+ * w4_kv8_free     the sequences seqs[0..n) end: their pages' refs drop by one,
+ *     their table rows become -1 and their lengths 0. A sequence listed twice
+ *     ends once; an empty one stays empty. (Not all or nothing: bad sequence or
+ *     page numbers are skipped and reported.)
+ * w4_kv8_compact  moves the pages in use to the front: with u pages in use,
+ *     those numbered u and above go, in ascending order, to the free numbers
+ *     below u, in ascending order. Rewrites refs and table and lists the moves
+ *     in copy_src / copy_dst [num_pages] (-1 after the last).
+ * w4_kv8_copy_pages  copies page src[i] to page dst[i], codes and scales, for
+ *     i < n (device arrays; an entry below 0 is skipped). No dst may appear
+ *     among the src entries or twice.
+ */
+W4_API size_t w4_kv8_pages_workspace_size(int num_pages, int n);
+W4_API w4_status w4_kv8_reserve(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                                int32_t* lens, int num_seqs, const int32_t* new_tokens,
+                                int page_size, int32_t* status_out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+W4_API w4_status w4_kv8_fork(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                             int32_t* lens, int num_seqs, const int32_t* src, const int32_t* dst,
+                             int n, int page_size, int32_t* copy_src, int32_t* copy_dst,
+                             int32_t* status_out, void* workspace, size_t workspace_bytes,
+                             void* stream);
+W4_API w4_status w4_kv8_free(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                             int32_t* lens, int num_seqs, const int32_t* seqs, int n,
+                             int page_size, int32_t* status_out, void* stream);
+W4_API w4_status w4_kv8_compact(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                                int num_seqs, int32_t* copy_src, int32_t* copy_dst,
+                                void* workspace, size_t workspace_bytes, void* stream);
+W4_API w4_status w4_kv8_copy_pages(const w4_kv8_cache* cache, const int32_t* src,
+                                   const int32_t* dst, int n, void* stream);
 
 #ifdef __cplusplus
 }

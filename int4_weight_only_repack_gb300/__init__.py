@@ -24,6 +24,9 @@ __all__ = [
     "w4_device_status", "w4_test_stalled_gemm", "w4_test_prefill_plan",
     "RepackedLayer", "repack_awq", "repack_gptq", "linear", "w4a16_moe_gemm", "RepackedExperts",
     "repack_awq_experts", "moe_linear",
+    "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "w4_kv8_attention_workspace_size",
+    "KV8Pool", "kv8_pool", "kv8_reserve", "kv8_fork", "kv8_free", "kv8_compact", "kv8_copy_pages",
+    "w4_kv8_pages_workspace_size",
 ]
 
 W4_F16, W4_BF16 = 0, 1
@@ -37,6 +40,19 @@ library_path = os.path.join(_PKG_DIR, "libw4a16.so")
 _LIB: Optional[ctypes.CDLL] = None
 
 _c_int, _c_size, _c_void_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+
+class _KV8CacheStruct(ctypes.Structure):
+    """w4_kv8_cache."""
+    _fields_ = [("k", _c_void_p), ("v", _c_void_p), ("k_scale", _c_void_p),
+                ("v_scale", _c_void_p), ("num_pages", _c_int), ("page_size", _c_int),
+                ("kv_heads", _c_int), ("head_dim", _c_int)]
+
+
+class _KV8HeadsStruct(ctypes.Structure):
+    """w4_kv8_heads."""
+    _fields_ = [("q_heads", _c_int), ("causal", _c_int), ("scale", ctypes.c_float)]
+
+
 _SIGNATURES = {
     "w4_status_string": (ctypes.c_char_p, [_c_int]),
     "w4_last_cuda_error": (ctypes.c_char_p, []),
@@ -70,6 +86,23 @@ _SIGNATURES = {
     "w4a8_gemm_workspace_size": (_c_size, [_c_int, _c_int]),
     "w4a8_gemm": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int,
                            _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_append": (_c_int, [_c_void_p, _c_void_p, _c_size, _c_size, _c_void_p, _c_void_p, _c_int,
+                               _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p]),
+    "w4_kv8_attention_workspace_size": (_c_size, [_c_int] * 7),
+    "w4_kv8_attention": (_c_int, [_c_void_p, _c_size, _c_void_p, _c_void_p, _c_int, _c_void_p,
+                                  _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                  _c_void_p, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_pages_workspace_size": (_c_size, [_c_int, _c_int]),
+    "w4_kv8_reserve": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int,
+                                _c_void_p, _c_int, _c_void_p, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_fork": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                             _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
+                             _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_free": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                             _c_int, _c_int, _c_void_p, _c_void_p]),
+    "w4_kv8_compact": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_int, _c_void_p,
+                                _c_void_p, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_copy_pages": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p]),
 }
 
 
@@ -415,3 +448,209 @@ def linear(x, layer: RepackedLayer, y=None, workspace=None, stream=None, bias=No
                                  y.data_ptr(), M, layer.N, layer.K, layer.group,
                                  dtype_code(layer.dtype), _ptr(workspace), ws_bytes, handle))
     return y
+
+
+# --------------------------------------------------------------------------- #
+# 8-bit key-value cache                                                         #
+# --------------------------------------------------------------------------- #
+class KV8Cache:
+    """One layer's cache: k and v float8_e4m3fn [pages, kv_heads, page, head_dim],
+    k_scale and v_scale float32 [pages, kv_heads], all contiguous on the GPU."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4 or v.shape != k.shape or k.dtype is not torch.float8_e4m3fn or \
+                v.dtype is not torch.float8_e4m3fn:
+            raise ValueError("k and v must be float8_e4m3fn [pages, kv_heads, page, head_dim]")
+        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or \
+                k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+            raise ValueError("k_scale and v_scale must be float32 [pages, kv_heads]")
+        if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            raise ValueError("the cache's tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self._struct = _KV8CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), self.num_pages, self.page_size,
+                                       self.kv_heads, self.head_dim)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def kv8_cache(num_pages, kv_heads, page_size, head_dim, device="cuda") -> KV8Cache:
+    """An empty cache."""
+    shape = (num_pages, kv_heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    return KV8Cache(k, v, ks, vs)
+
+
+def _rows(x, name, heads, dim):
+    """The token stride of x [tokens, heads, dim], whose rows may be slices of a
+    wider buffer but whose heads and elements are adjacent."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {tuple(x.shape)}")
+    st = x.stride()
+    if x.shape[0] and (st[2] != 1 or (st[1] != dim and heads > 1)):
+        raise ValueError(f"{name}: heads and elements of a token must be adjacent in memory")
+    return st[0] if x.shape[0] > 1 else heads * dim
+
+
+def _ints(x, name):
+    """Checks an int32 array: contiguous but for the row stride of a matrix."""
+    if x.dtype is not torch.int32 or (x.stride(-1) != 1 and x.shape[-1] > 1):
+        raise ValueError(f"{name} must be int32 with adjacent elements")
+    return x.data_ptr()
+
+
+def _table_stride(table):
+    if table.dim() != 2:
+        raise ValueError("the table must be [sequences, pages]")
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=None):
+    """Quantises new keys and values k, v [tokens, kv_heads, head_dim] (fp16 or
+    bf16, packed by sequence: rows cu_q[b] .. cu_q[b + 1]) into the cache as each
+    sequence's last tokens: kv_lens [batch] counts them already. table [batch,
+    pages] int32 gives the sequences' pages. See w4_kv8_append in include/w4a16.h."""
+    if v.dtype is not k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must have the same type and shape")
+    hk, d = cache.kv_heads, cache.head_dim
+    _check(lib().w4_kv8_append(
+        k.data_ptr(), v.data_ptr(), _rows(k, "k", hk, d), _rows(v, "v", hk, d), cache._ref,
+        _ints(table, "table"), _table_stride(table), _ints(kv_lens, "kv_lens"),
+        _ints(cu_q, "cu_q"), _batch(table, kv_lens, cu_q), k.shape[0], max_q_len,
+        dtype_code(k.dtype), _stream(stream, k.device.index)))
+
+
+def _batch(table, kv_lens, cu_q):
+    b = kv_lens.shape[0]
+    if table.shape[0] < b or cu_q.shape[0] != b + 1:
+        raise ValueError("table needs a row and cu_q a bound for every entry of kv_lens")
+    return b
+
+
+def w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_heads, kv_heads,
+                                    head_dim) -> int:
+    return lib().w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_heads,
+                                                 kv_heads, head_dim)
+
+
+def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_len, scale=None,
+                  causal=True, out=None, workspace=None, stream=None):
+    """Attention of q [tokens, q_heads, head_dim] (fp16 or bf16, packed by
+    sequence as for kv8_append) over each sequence's kv_lens[b] cached tokens;
+    causal: its queries are its last tokens; otherwise each sees all of them.
+    scale defaults to head_dim ** -0.5. Without `workspace`, the one kept for
+    (device, stream) is used. See w4_kv8_attention in include/w4a16.h."""
+    tokens, heads, dim = q.shape
+    stride = _rows(q, "q", heads, cache.head_dim)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with q's shape and type")
+    batch = _batch(table, kv_lens, cu_q)
+    if heads % cache.kv_heads:
+        raise W4Error(2, w4_status_string(2))
+    how = _KV8HeadsStruct(heads, causal, dim ** -0.5 if scale is None else scale)
+    L = lib()
+    nbytes = L.w4_kv8_attention_workspace_size(batch, tokens, max_q_len, max_kv_len, heads,
+                                               cache.kv_heads, dim)
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    elif nbytes:
+        workspace = gemm_workspace(nbytes, q.device, stream)
+    _check(L.w4_kv8_attention(
+        q.data_ptr(), stride, cache._ref, _ints(table, "table"), _table_stride(table),
+        _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len,
+        max_kv_len, ctypes.addressof(how), dtype_code(q.dtype),
+        None if workspace is None else workspace.data_ptr(), nbytes,
+        _stream(stream, q.device.index)))
+    return out
+
+
+class KV8Pool:
+    """The pages of a pool and the sequences that hold them: refs [pages] (0: a
+    free page), table [sequences, pages of the longest] (-1 past a sequence's
+    pages), lens [sequences] (tokens; 0: an empty slot), int32 on the GPU.
+    status: an int32 tensor that receives each call's W4_OK or error (a call
+    that fails changes nothing); without one, errors go to w4_device_status."""
+
+    def __init__(self, refs, table, lens, page_size, status=None):
+        if table.dim() != 2 or table.shape[0] != lens.shape[0]:
+            raise ValueError("table must be [sequences, pages], lens [sequences]")
+        self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
+        self.status = status
+        self._args = (_ints(refs, "refs"), refs.shape[0], _ints(table, "table"),
+                      _table_stride(table), _ints(lens, "lens"), lens.shape[0])
+        self._status = None if status is None else _ints(status, "status")
+
+    def _workspace(self, n, stream):
+        nbytes = lib().w4_kv8_pages_workspace_size(self.refs.shape[0], n)
+        return gemm_workspace(nbytes, self.refs.device, stream).data_ptr(), nbytes
+
+
+def kv8_pool(num_pages, num_seqs, max_len, page_size, device="cuda") -> KV8Pool:
+    """A pool of free pages with num_seqs empty sequences of at most max_len tokens."""
+    return KV8Pool(torch.zeros(num_pages, dtype=torch.int32, device=device),
+                   torch.full((num_seqs, -(-max_len // page_size)), -1, dtype=torch.int32,
+                              device=device),
+                   torch.zeros(num_seqs, dtype=torch.int32, device=device), page_size,
+                   torch.zeros(1, dtype=torch.int32, device=device))
+
+
+def w4_kv8_pages_workspace_size(num_pages, n) -> int:
+    return lib().w4_kv8_pages_workspace_size(num_pages, n)
+
+
+def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
+    """Lengthens every sequence s by new_tokens[s] and gives it the pages that
+    takes, the lowest free ones in order."""
+    if new_tokens.shape != pool.lens.shape:
+        raise ValueError("new_tokens must have an entry for every sequence")
+    ws, nbytes = pool._workspace(pool.lens.shape[0], stream)
+    _check(lib().w4_kv8_reserve(*pool._args, _ints(new_tokens, "new_tokens"), pool.page_size,
+                                pool._status, ws, nbytes,
+                                _stream(stream, pool.refs.device.index)))
+
+
+def kv8_fork(pool: KV8Pool, src, dst, stream=None):
+    """Makes each empty sequence dst[i] a copy of src[i] that shares its full
+    pages. Returns (copy_src, copy_dst): the last partial pages to copy with
+    kv8_copy_pages in every layer's cache (-1 where there is none)."""
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError("src and dst must have the same length")
+    moves = torch.empty((2, n), dtype=torch.int32, device=pool.refs.device)
+    ws, nbytes = pool._workspace(n, stream)
+    copy_src, copy_dst = moves[0], moves[1]
+    _check(lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n, pool.page_size,
+                             copy_src.data_ptr(), copy_dst.data_ptr(), pool._status, ws, nbytes,
+                             _stream(stream, pool.refs.device.index)))
+    return copy_src, copy_dst
+
+
+def kv8_free(pool: KV8Pool, seqs, stream=None):
+    """Ends the sequences: their pages lose a reference, their slots become empty."""
+    _check(lib().w4_kv8_free(*pool._args, _ints(seqs, "seqs"), seqs.shape[0], pool.page_size,
+                             pool._status, _stream(stream, pool.refs.device.index)))
+
+
+def kv8_compact(pool: KV8Pool, stream=None):
+    """Renumbers the pages in use to the front of the pool. Returns (copy_src,
+    copy_dst) for kv8_copy_pages in every layer's cache (-1 after the last)."""
+    moves = torch.empty((2, pool.refs.shape[0]), dtype=torch.int32, device=pool.refs.device)
+    ws, nbytes = pool._workspace(pool.lens.shape[0], stream)
+    copy_src, copy_dst = moves[0], moves[1]
+    _check(lib().w4_kv8_compact(*pool._args[:4], pool._args[5], copy_src.data_ptr(),
+                                copy_dst.data_ptr(), ws, nbytes,
+                                _stream(stream, pool.refs.device.index)))
+    return copy_src, copy_dst
+
+
+def kv8_copy_pages(cache: KV8Cache, src, dst, stream=None):
+    """Copies page src[i] to page dst[i], codes and scales (entries below 0: none)."""
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _check(lib().w4_kv8_copy_pages(cache._ref, _ints(src, "src"), _ints(dst, "dst"), src.shape[0],
+                                   _stream(stream, cache.k.device.index)))

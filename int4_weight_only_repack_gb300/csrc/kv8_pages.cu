@@ -1,0 +1,488 @@
+// Pages of the 8-bit key-value cache: reserve, fork, free, compact, copy.
+//
+// The reference counts are the only record of which pages are free. "The
+// lowest free pages, in order" is a stream compaction of refs == 0, so the
+// results never depend on the order in which threads arrive. A pool has some
+// thousand to a million pages (4 MB of counts at most), too few to fill the
+// GPU and bound by latency, so each call is ONE launch of one cluster of
+// eight CTAs: 256 warps each take a contiguous chunk of pages and count by
+// ballot, the counts are exchanged through distributed shared memory, and
+// every warp then knows the rank of its pages. Only the copy of the pages
+// themselves, bound by HBM, is a grid over the whole GPU.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kv8_device.cuh"
+
+namespace w4 {
+namespace kv8 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int CL = 8;              // CTAs of the cluster (the portable maximum)
+constexpr int BT = 1024;           // threads of a CTA
+constexpr int BW = BT / 32;        // warps of a CTA
+constexpr int NW = CL * BW;        // warps of the cluster
+
+struct Book {
+  int32_t *refs, *table, *lens;
+  int pages, stride, seqs, shift;
+  const int32_t *list, *list2;
+  int n;
+  int32_t *copy_src, *copy_dst;
+  int32_t* status_out;  // or nullptr
+  int* status;          // the library's device status word
+  int32_t* ws;
+};
+
+// Per-warp counts of the cluster, exchanged once: [0] pages, [1] pages needed.
+struct Counts {
+  int own[2][BW];   // this CTA's warps
+  int before[2][BW];  // what the cluster's warps before each of them counted
+  int total[2];
+  int err;          // this CTA's error, then the cluster's
+};
+
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
+__device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
+__device__ __forceinline__ unsigned lanes_below() { return (1u << lane_id()) - 1u; }
+
+// The chunk [lo, hi) of n items that cluster warp w takes: whole 32s.
+__device__ __forceinline__ void chunk(int n, int w, int* lo, int* hi) {
+  const int per = ((n + NW - 1) / NW + 31) & ~31;
+  *lo = min(n, w * per);
+  *hi = min(n, *lo + per);
+}
+
+// Exchange the warps' counts: every CTA reads all 256 of both kinds (warp 0:
+// pages, warp 1: needs), sums what lies before its own warps and in all.
+__device__ void exchange(cg::cluster_group& cl, Counts& c) {
+  cl.sync();
+  const int rank = (int)cl.block_rank(), w = warp_id(), lane = lane_id();
+  if (w < 2) {
+    int run = 0;
+    for (int r = 0; r < CL; ++r) {
+      const Counts* o = cl.map_shared_rank(&c, r);
+      const int v = o->own[w][lane];
+      int inc = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(~0u, inc, d);
+        if (lane >= d) inc += u;
+      }
+      if (r == rank) c.before[w][lane] = run + inc - v;
+      run += __shfl_sync(~0u, inc, 31);
+    }
+    if (lane == 0) c.total[w] = run;
+  }
+  __syncthreads();
+}
+
+// Whether any CTA of the cluster has seen an error (the largest code wins).
+__device__ int cluster_error(cg::cluster_group& cl, Counts& c) {
+  cl.sync();
+  int e = 0;
+  for (int r = 0; r < CL; ++r) e = max(e, cl.map_shared_rank(&c, r)->err);
+  return e;
+}
+
+__device__ void report(const Book& b, int err) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (b.status_out) *b.status_out = err;
+    else if (err) record(b.status, err);
+  }
+}
+
+// Count this warp's free (or live) pages into c.own[0].
+template <bool LIVE>
+__device__ void count_pages(const Book& b, Counts& c) {
+  int lo, hi, n = 0;
+  chunk(b.pages, blockIdx.x * BW + warp_id(), &lo, &hi);
+#pragma unroll 4
+  for (int p = lo + lane_id(); p < hi; p += 32) n += (b.refs[p] > 0) == LIVE;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(~0u, n, d);
+  if (lane_id() == 0) c.own[0][warp_id()] = n;
+}
+
+// List the first `want` free pages in order and take them (refs = 1).
+__device__ void take_pages(const Book& b, const Counts& c, int32_t* fresh, int want) {
+  int lo, hi;
+  chunk(b.pages, blockIdx.x * BW + warp_id(), &lo, &hi);
+  int rank = c.before[0][warp_id()];
+  for (int base = lo; base < hi && rank < want; base += 32) {
+    const int p = base + lane_id();
+    const bool free = p < hi && b.refs[p] <= 0;
+    const unsigned m = __ballot_sync(~0u, free);
+    const int r = rank + __popc(m & lanes_below());
+    if (free && r < want) {
+      fresh[r] = p;
+      b.refs[p] = 1;
+    }
+    rank += __popc(m);
+  }
+}
+
+__device__ __forceinline__ int pages_of(long long tokens, int shift) {
+  return (int)((tokens + (1ll << shift) - 1) >> shift);
+}
+
+__global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(const Book b) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Counts c;
+  grid_wait();
+  grid_launch_dependents();
+  const int w = blockIdx.x * BW + warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) c.err = 0;
+  __syncthreads();
+  count_pages<false>(b, c);
+  int lo, hi, need = 0;
+  chunk(b.seqs, w, &lo, &hi);
+  for (int s = lo + lane; s < hi; s += 32) {
+    const int held = b.lens[s], add = b.list[s];
+    const long long sum = (long long)held + add;
+    if (held < 0 || add < 0 || sum > ((long long)b.stride << b.shift))
+      atomicMax(&c.err, W4_ERR_PAGE);
+    else
+      need += pages_of(sum, b.shift) - pages_of(held, b.shift);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) need += __shfl_xor_sync(~0u, need, d);
+  if (lane == 0) c.own[1][warp_id()] = need;
+  __syncthreads();
+  int err = cluster_error(cl, c);
+  exchange(cl, c);
+  const int want = c.total[1];
+  if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
+  report(b, err);
+  if (!err) take_pages(b, c, b.ws, want);
+  cl.sync();  // the list is complete (and no CTA leaves while its counts are read)
+  if (err) return;
+  int off = c.before[1][warp_id()];
+  for (int base = lo; base < hi; base += 32) {
+    const int s = base + lane;
+    int have = 0, n = 0;
+    if (s < hi) {
+      const int held = b.lens[s], add = b.list[s];
+      have = pages_of(held, b.shift);
+      n = pages_of((long long)held + add, b.shift) - have;
+      if (add) b.lens[s] = held + add;
+    }
+    unsigned todo = __ballot_sync(~0u, n > 0);
+    while (todo) {  // the warp writes one sequence's new pages at a time
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int m = __shfl_sync(~0u, n, l), at = __shfl_sync(~0u, have, l);
+      int32_t* row = b.table + (size_t)(base + l) * b.stride + at;
+      for (int j = lane; j < m; j += 32) row[j] = b.ws[off + j];
+      off += m;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(const Book b) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Counts c;
+  grid_wait();
+  grid_launch_dependents();
+  int32_t* fresh = b.ws;
+  int32_t* offs = b.ws + b.pages;  // per pair: rank of its fresh page, -1 for none
+  int32_t* held = offs + b.n;      // per pair: the source's tokens
+  const int w = blockIdx.x * BW + warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) c.err = 0;
+  __syncthreads();
+  count_pages<false>(b, c);
+  int lo, hi, need = 0;
+  chunk(b.n, w, &lo, &hi);
+  for (int base = lo; base < hi; base += 32) {
+    const int i = base + lane;
+    int part = 0, toks = 0;
+    if (i < hi) {
+      const int s = b.list[i], d = b.list2[i];
+      if (s < 0 || s >= b.seqs || d < 0 || d >= b.seqs) {
+        atomicMax(&c.err, W4_ERR_SEQ);
+      } else {
+        toks = b.lens[s];
+        if (toks < 0 || toks > ((long long)b.stride << b.shift)) {
+          atomicMax(&c.err, W4_ERR_PAGE);
+          toks = 0;
+        }
+        part = (toks & ((1 << b.shift) - 1)) != 0;
+      }
+      held[i] = toks;
+    }
+    const unsigned m = __ballot_sync(~0u, part != 0);
+    if (i < hi) offs[i] = part ? need + __popc(m & lanes_below()) : -1;  // + the warp's own start
+    need += __popc(m);
+  }
+  if (lane == 0) c.own[1][warp_id()] = need;
+  // the sources' page numbers, one warp a pair
+  for (int i = w; i < b.n; i += NW) {
+    const int s = b.list[i];
+    if (s < 0 || s >= b.seqs) continue;
+    const int n = min(pages_of(max(b.lens[s], 0), b.shift), b.stride);
+    for (int j = lane; j < n; j += 32) {
+      const int p = b.table[(size_t)s * b.stride + j];
+      if (p < 0 || p >= b.pages) atomicMax(&c.err, W4_ERR_PAGE);
+    }
+  }
+  __syncthreads();
+  int err = cluster_error(cl, c);
+  exchange(cl, c);
+  const int want = c.total[1];
+  if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
+  // claim the targets: each must be empty, and only one pair's
+  if (!err) {
+    for (int i = lo + lane; i < hi; i += 32)
+      if (atomicCAS(&b.lens[b.list2[i]], 0, -(i + 1)) != 0) atomicMax(&c.err, W4_ERR_SEQ);
+    __syncthreads();
+    err = cluster_error(cl, c);
+    if (err)
+      for (int i = lo + lane; i < hi; i += 32) atomicCAS(&b.lens[b.list2[i]], -(i + 1), 0);
+  }
+  report(b, err);
+  if (!err) {
+    take_pages(b, c, fresh, want);
+    for (int i = lo + lane; i < hi; i += 32)
+      if (offs[i] >= 0) offs[i] += c.before[1][warp_id()];
+  }
+  cl.sync();
+  if (err) return;
+  for (int i = w; i < b.n; i += NW) {  // one warp a pair
+    const int s = b.list[i], d = b.list2[i], toks = held[i], off = offs[i];
+    const int full = toks >> b.shift;
+    const int32_t* from = b.table + (size_t)s * b.stride;
+    int32_t* to = b.table + (size_t)d * b.stride;
+    const int page = off >= 0 ? fresh[off] : -1;
+    const int last = off >= 0 ? from[full] : -1;
+    for (int j = lane; j < b.stride; j += 32) {
+      int p = -1;
+      if (j < full) {
+        p = from[j];
+        atomicAdd(&b.refs[p], 1);
+      } else if (j == full) {
+        p = page;
+      }
+      to[j] = p;
+    }
+    if (lane == 0) {
+      b.lens[d] = toks;
+      b.copy_src[i] = last;
+      b.copy_dst[i] = page;
+    }
+  }
+}
+
+// One CTA a listed sequence. The exchange of its length decides which of two
+// entries of the same sequence ends it, so its pages drop by one exactly once.
+__global__ void __launch_bounds__(128) free_kernel(const Book b) {
+  __shared__ int toks_sh;
+  grid_wait();
+  grid_launch_dependents();
+  int* status = b.status_out ? b.status_out : b.status;
+  const int s = b.list[blockIdx.x];
+  if (s < 0 || s >= b.seqs) {
+    if (threadIdx.x == 0) record(status, W4_ERR_SEQ);
+    return;
+  }
+  if (threadIdx.x == 0) toks_sh = atomicExch(&b.lens[s], 0);
+  __syncthreads();
+  const long long toks = toks_sh;
+  if (toks == 0) return;
+  if (toks < 0 || toks > ((long long)b.stride << b.shift)) {
+    if (threadIdx.x == 0) record(status, W4_ERR_PAGE);
+    return;
+  }
+  const int n = pages_of(toks, b.shift);
+  int32_t* row = b.table + (size_t)s * b.stride;
+  for (int j = threadIdx.x; j < b.stride; j += blockDim.x) {
+    const int p = row[j];
+    row[j] = -1;
+    if (j >= n) continue;
+    if (p < 0 || p >= b.pages) {
+      record(status, W4_ERR_PAGE);
+    } else if (atomicSub(&b.refs[p], 1) <= 0) {  // it was free already: leave it so
+      atomicAdd(&b.refs[p], 1);
+      record(status, W4_ERR_PAGE);
+    }
+  }
+}
+
+__global__ void clear_status_kernel(int32_t* status) {
+  grid_wait();
+  grid_launch_dependents();
+  *status = W4_OK;
+}
+
+// ws: [0] pages in use, [16 + p] the page that p becomes (p at or above that number).
+constexpr int MAP_AT = 16;
+
+__global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) compact_kernel(const Book b) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ Counts c;
+  __shared__ int holes_sh;
+  grid_wait();
+  grid_launch_dependents();
+  const int w = blockIdx.x * BW + warp_id(), lane = lane_id();
+  if (lane == 0) c.own[1][warp_id()] = 0;
+  if (threadIdx.x == 0) holes_sh = 0;
+  count_pages<true>(b, c);
+  __syncthreads();
+  exchange(cl, c);
+  const int used = c.total[0];
+  int lo, hi;
+  chunk(b.pages, w, &lo, &hi);
+  int n = c.before[0][warp_id()];  // live pages before this chunk
+  // holes: free pages below `used`. Whoever has page `used` in its chunk knows
+  // how many live ones lie below it (with used == pages there are none).
+  if (used >= lo && used < hi) {
+    int k = 0;
+    for (int p = lo + lane; p < used; p += 32) k += b.refs[p] > 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) k += __shfl_xor_sync(~0u, k, d);
+    if (lane < CL) *cl.map_shared_rank(&holes_sh, lane) = used - (n + k);
+  }
+  cl.sync();
+  const int holes = holes_sh;
+  for (int base = lo; base < hi; base += 32) {
+    const int p = base + lane;
+    const bool live = p < hi && b.refs[p] > 0;
+    const unsigned m = __ballot_sync(~0u, live);
+    const int before = n + __popc(m & lanes_below());
+    if (p < hi) {
+      if (p < used) {
+        if (!live) b.copy_dst[p - before] = p;
+      } else {
+        b.ws[MAP_AT + p] = p;
+        if (live) b.copy_src[before - (used - holes)] = p;
+      }
+    }
+    n += __popc(m);
+  }
+  const int at = blockIdx.x * BT + threadIdx.x;
+  for (int i = holes + at; i < b.pages; i += CL * BT) b.copy_src[i] = b.copy_dst[i] = -1;
+  if (at == 0) b.ws[0] = used;
+  cl.sync();
+  for (int i = at; i < holes; i += CL * BT) {
+    const int s = b.copy_src[i], d = b.copy_dst[i];
+    b.refs[d] = b.refs[s];
+    b.refs[s] = 0;
+    b.ws[MAP_AT + s] = d;
+  }
+}
+
+__global__ void __launch_bounds__(256) retable_kernel(int32_t* table, size_t entries,
+                                                      const int32_t* ws, int pages) {
+  grid_wait();
+  grid_launch_dependents();
+  const int used = ws[0];
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < entries; i += (size_t)gridDim.x * 256) {
+    const int p = table[i];
+    if (p >= used && p < pages) table[i] = ws[MAP_AT + p];
+  }
+}
+
+// One page's codes are one run in memory (keys and values each), cut into
+// pieces of 16 KB: 256 threads move a piece with four 16-byte loads in flight
+// each. Pieces are spread over the grid page by page, so the -1 entries at a
+// list's end leave no CTA with more work than another.
+constexpr int CT = 256, CU = 4, PIECE = CT * CU * 16;
+
+__global__ void __launch_bounds__(CT) copy_kernel(const Cache c, size_t page_bytes,
+                                                  const int32_t* src, const int32_t* dst, int n,
+                                                  int pieces, int* status) {
+  grid_wait();
+  grid_launch_dependents();
+  const long long units = (long long)n * 2 * pieces;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int i = (int)(u / (2 * pieces)), r = (int)(u - (long long)i * 2 * pieces);
+    const int s = src[i], d = dst[i];
+    if (s < 0 || d < 0) continue;
+    if (s >= c.pages || d >= c.pages) {
+      if (threadIdx.x == 0) record(status, W4_ERR_PAGE);
+      continue;
+    }
+    const int piece = r >> 1;
+    uint8_t* base = (r & 1) ? c.v : c.k;
+    const uint4* from = reinterpret_cast<const uint4*>(base + s * page_bytes + (size_t)piece * PIECE);
+    uint4* to = reinterpret_cast<uint4*>(base + d * page_bytes + (size_t)piece * PIECE);
+    const int left = (int)(min((size_t)PIECE, page_bytes - (size_t)piece * PIECE) / 16);
+    uint4 x[CU];
+#pragma unroll
+    for (int j = 0; j < CU; ++j)
+      if (threadIdx.x + j * CT < left) x[j] = __ldcs(from + threadIdx.x + j * CT);
+#pragma unroll
+    for (int j = 0; j < CU; ++j)
+      if (threadIdx.x + j * CT < left) __stcs(to + threadIdx.x + j * CT, x[j]);
+    if (piece == 0) {
+      float* sc = (r & 1) ? c.vs : c.ks;
+      for (int h = threadIdx.x; h < c.heads; h += CT)
+        sc[(size_t)d * c.heads + h] = sc[(size_t)s * c.heads + h];
+    }
+  }
+}
+
+Book book(const BookArgs& a, int* status) {
+  return {a.refs, a.table, a.lens, a.pages, a.table_stride, a.seqs, a.page_shift, a.list, a.list2,
+          a.n, a.copy_src, a.copy_dst, a.status_out, status, static_cast<int32_t*>(a.workspace)};
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(int num_pages, int n) {
+  return ((size_t)num_pages + 2 * (size_t)n + 64) * 4;
+}
+
+cudaError_t launch_reserve(const BookArgs& a, cudaStream_t s) {
+  int* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
+  return launch(reserve_kernel, dim3(CL), BT, 0, s, book(a, status));
+}
+
+cudaError_t launch_fork(const BookArgs& a, cudaStream_t s) {
+  int* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
+  return launch(fork_kernel, dim3(CL), BT, 0, s, book(a, status));
+}
+
+cudaError_t launch_free(const BookArgs& a, cudaStream_t s) {
+  int* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
+  if (a.status_out && (e = launch(clear_status_kernel, dim3(1), 1, 0, s, a.status_out)) != cudaSuccess)
+    return e;
+  if (a.n == 0) return cudaSuccess;
+  return launch(free_kernel, dim3(a.n), 128, 0, s, book(a, status));
+}
+
+cudaError_t launch_compact(const BookArgs& a, cudaStream_t s) {
+  cudaError_t e = launch(compact_kernel, dim3(CL), BT, 0, s, book(a, nullptr));
+  if (e != cudaSuccess || a.seqs == 0) return e;
+  DeviceInfo info;
+  if ((e = device_info(&info)) != cudaSuccess) return e;
+  const size_t entries = (size_t)a.seqs * a.table_stride;
+  const int grid = (int)std::min<size_t>((entries + 255) / 256, (size_t)info.sm_count * 8);
+  return launch(retable_kernel, dim3(grid), 256, 0, s, a.table, entries,
+                static_cast<const int32_t*>(a.workspace), a.pages);
+}
+
+cudaError_t launch_copy_pages(const Cache& c, int dim, const int32_t* src, const int32_t* dst,
+                              int n, cudaStream_t s) {
+  int* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
+  DeviceInfo info;
+  if ((e = device_info(&info)) != cudaSuccess) return e;
+  const size_t page_bytes = ((size_t)c.heads * dim) << c.page_shift;
+  const int pieces = (int)((page_bytes + PIECE - 1) / PIECE);
+  const long long units = (long long)n * 2 * pieces;
+  const int grid = (int)std::min<long long>(units, (long long)info.sm_count * 8);
+  return launch(copy_kernel, dim3(grid), CT, 0, s, c, page_bytes, src, dst, n, pieces, status);
+}
+
+}  // namespace kv8
+}  // namespace w4

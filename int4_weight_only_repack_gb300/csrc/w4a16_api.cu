@@ -16,14 +16,6 @@ constexpr int MAX_DIM = 1 << 20;
 constexpr int MAX_DEVICES = 64;
 constexpr int MAX_ACT_ORDER_GROUPS = 8192;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 bool valid_group(int group) { return group == -1 || group == 32 || group == 64 || group == 128; }
 
 int resolve_group(int group, int K) { return group == -1 ? K : group; }
@@ -54,14 +46,6 @@ struct CachedInfo {
 CachedInfo g_info[MAX_DEVICES];
 std::mutex g_info_mu;
 
-// The current device must be compute capability 10.3 (the kernels are sm_103a only).
-w4_status check_arch() {
-  DeviceInfo info;
-  if (device_info(&info) != cudaSuccess) return W4_ERR_CUDA;
-  if (info.major != 10 || info.minor != 3) return W4_ERR_ARCH;
-  return W4_OK;
-}
-
 // The last CUDA error an entry point reported on this thread (w4_last_cuda_error).
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
@@ -71,13 +55,20 @@ w4_status gemm_impl(const void* x, const int32_t* qw, const void* scales, const 
                     int group, int dtype, void* workspace, size_t workspace_bytes, void* stream,
                     int test_stall);
 
+}  // namespace
+
 w4_status from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return W4_OK;
   g_last_cuda_error = e;
   return W4_ERR_CUDA;
 }
 
-}  // namespace
+w4_status check_arch() {
+  DeviceInfo info;
+  if (device_info(&info) != cudaSuccess) return W4_ERR_CUDA;
+  if (info.major != 10 || info.minor != 3) return W4_ERR_ARCH;
+  return W4_OK;
+}
 
 cudaError_t device_info(DeviceInfo* out) {
   int dev = 0;
@@ -129,6 +120,9 @@ const char* w4_status_string(w4_status s) {
     case W4_ERR_TIMEOUT: return "W4_ERR_TIMEOUT: a kernel gave up on a pipeline wait";
     case W4_ERR_EXPERT_ROWS:
       return "W4_ERR_EXPERT_ROWS: an expert's rows were invalid or more than max_rows_per_expert";
+    case W4_ERR_PAGE: return "W4_ERR_PAGE: a page number, length or offset on the device is out of range";
+    case W4_ERR_NO_PAGES: return "W4_ERR_NO_PAGES: too few free pages";
+    case W4_ERR_SEQ: return "W4_ERR_SEQ: a sequence number is out of range, or a fork's target is not empty";
     default: return "unknown w4_status";
   }
 }

@@ -127,4 +127,16 @@ struct DeviceInfo {
 };
 cudaError_t device_info(DeviceInfo* out);
 
+// Checks the entry points share: pointer alignment, overlap of two buffers, the
+// current device's compute capability (10.3: the kernels are sm_103a only), and
+// the status of a CUDA error (kept for w4_last_cuda_error).
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+w4_status check_arch();
+w4_status from_cuda(cudaError_t e);
+
 }  // namespace w4
