@@ -1,0 +1,95 @@
+// Device code shared by the two attention kernels of the 8-bit cache.
+//
+//   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),
+//   k_j = kc_j ks, v_j = vc_j vs  (ks, vs: one scale per page and head).
+//
+// One pass over the cache with a running maximum. With x_j = log2(e) scale ks
+// (q . kc_j) + log2(vs) the running maximum is m = max x_j, p'_j = 2^(x_j - m),
+// and
+//   O = sum_j p'_j vc_j,   l = sum_j p'_j / vs,   out = O / l:
+// the values' scale enters the exponent, so the codes themselves are the
+// operand of the second product and p' <= 1 fits fp16.
+//
+// The q_heads / kv_heads query heads that share a kv head, and the new tokens
+// of a sequence, are rows of one item: row r is token r / group, head r % group.
+#pragma once
+
+#include "kv8_device.cuh"
+
+namespace w4 {
+namespace kv8 {
+
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+struct Attn {
+  const uint16_t* q;
+  size_t q_stride;
+  Cache c;
+  const int32_t *table, *kv_lens, *cu_q;
+  uint16_t* out;
+  int table_stride, batch, total_q, max_q, max_kv, q_heads, group, causal;
+  float scale_log2;  // scale * log2(e)
+  int* status;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float to_float(uint16_t h) {
+  if constexpr (BF16) return __uint_as_float((uint32_t)h << 16);
+  else return __half2float(__ushort_as_half(h));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+  uint32_t d;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return pack_out<false>(lo, hi); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Sets the NaN codes (0x7F, 0xFF) of four to zero; whether there were any.
+__device__ __forceinline__ bool zero_nan_codes(uint32_t& w) {
+  const uint32_t hit = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  if (hit == 0) return false;
+  w &= ~((hit >> 7) * 0xFFu);
+  return true;
+}
+
+// Sequence b of the batch, checked: rows of new tokens and cached tokens.
+struct Seq {
+  int q0, n, kv;
+  bool ok;
+};
+__device__ __forceinline__ Seq load_seq(const Attn& a, int b) {
+  Seq s;
+  s.q0 = a.cu_q[b];
+  s.n = a.cu_q[b + 1] - s.q0;
+  s.kv = a.kv_lens[b];
+  s.ok = s.q0 >= 0 && s.n >= 0 && s.n <= a.max_q && s.q0 <= a.total_q - s.n;
+  if (!s.ok) s.n = 0;
+  if (s.kv < 0 || s.kv > a.max_kv || s.kv > ((long long)a.table_stride << a.c.page_shift)) {
+    s.kv = 0;
+    s.ok = false;
+  }
+  return s;
+}
+
+}  // namespace kv8
+}  // namespace w4

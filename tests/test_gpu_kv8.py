@@ -454,3 +454,17 @@ def test_fork_compact_keep_what_sequences_hold(w4):
     assert torch.equal(after[[1, 2, 4]], now[[1, 2, 4]])
     assert torch.count_nonzero(after[[0, 3]]) == 0
     assert w4.w4_device_status() == 0
+
+
+def test_workspace_contents_do_not_matter(w4):
+    lens = [5000, 700, 2100, 33, 0]
+    cache = ref.random_cache(w4, 300, 4, 32, 128, seed=60)
+    table = ref.scattered_table(lens, 32, 300, seed=61)
+    size = w4.w4_kv8_attention_workspace_size(5, 5, 1, 5000, 8, 4, 128)
+    q = queries(5, 8, 128, "bf16", 62)
+    want = check(w4, q, cache, table, lens, [1] * 5, True, "bf16")
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got = w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds([1] * 5), 1, 5000,
+                               workspace=ws)
+        assert torch.equal(got, want)
