@@ -25,7 +25,6 @@
 //   Row c of an A operand's eight is token rho(c): rho spreads the rows that a
 //   phase of eight lanes reads over all banks of the swizzled tile.
 #include <algorithm>
-#include <mutex>
 
 #include "decode_common.cuh"
 #include "kv8_attention.cuh"
@@ -851,24 +850,13 @@ bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Which kernel a call runs.
+bool many_rows(int max_q, int group) { return (long long)max_q * group > 64; }
+
 bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX_SCAN; }
 
 // Rows of queries that share one widening of the codes, in eights.
 int row_blocks(long long rows) { return rows > 8 ? 2 : 1; }
-
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[64]) {
-  static std::mutex mu;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  done[dev] = e == cudaSuccess;
-  return e;
-}
 
 template <int D, int NB, bool BF16>
 cudaError_t launch_rows(Rows& r, int sms, cudaStream_t s) {
@@ -902,7 +890,7 @@ cudaError_t launch_d(Rows& r, int sms, cudaStream_t s) {
 
 size_t attention_workspace_bytes(int batch, int max_q, int max_kv, int q_heads, int kv_heads,
                                  int dim) {
-  if (!splits(batch, max_kv)) return 0;
+  if (many_rows(max_q, q_heads / kv_heads) || !splits(batch, max_kv)) return 0;
   const int nb = row_blocks((long long)max_q * (q_heads / kv_heads));
   return (size_t)MAX_WORKERS * sizeof(Begun) + (size_t)MAX_WORKERS * 2 * part_floats(dim, nb) * 4;
 }
@@ -917,6 +905,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s) {
   r.a = {a.q, a.q_stride, a.c, a.table, a.kv_lens, a.cu_q, a.out, a.table_stride, a.batch,
          a.total_q, a.max_q, a.max_kv, a.q_heads, a.q_heads / a.c.heads, a.causal,
          a.scale * 1.44269504088896340736f, status};
+  if (many_rows(a.max_q, r.a.group)) return launch_prompt(r.a, a.dim, a.bf16, s);
   const int box = std::min(1 << a.c.page_shift, STEP);
   if (!encode_rows(&r.tk, a.c.k, a.c, a.dim, box) || !encode_rows(&r.tv, a.c.v, a.c, a.dim, box))
     return cudaErrorInvalidValue;

@@ -32,6 +32,9 @@ struct Attn {
   int* status;
 };
 
+// The kernel for many rows (kv8_prompt.cu).
+cudaError_t launch_prompt(const Attn& a, int dim, int bf16, cudaStream_t s);
+
 template <bool BF16>
 __device__ __forceinline__ float to_float(uint16_t h) {
   if constexpr (BF16) return __uint_as_float((uint32_t)h << 16);
