@@ -34,7 +34,6 @@ namespace kv8 {
 namespace {
 
 using namespace sm100;
-using dec::bounded_wait;
 using dec::drain_wait;
 
 constexpr int WARPS = 4, THREADS = WARPS * 32, STEP = 32, STAGES = 2;
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     }
     for (int u = seg.u0 + phase; u < seg.u1; u += STRIDE) {
       const int st = it % STAGES, j0 = u * STEP;
-      if (ok) ok = __all_sync(~0u, bounded_wait(bars + 8 * st, (it / STAGES) & 1, abort_flag, a.status));
+      if (ok) ok = __all_sync(~0u, wait_for(bars + 8 * st, (it / STAGES) & 1, abort_flag, a.status));
       if (!ok) break;
       ++it;
       const uint32_t kt = ring + st * L::STAGE, vt = kt + L::TILE;

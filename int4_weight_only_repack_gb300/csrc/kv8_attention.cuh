@@ -14,12 +14,33 @@
 // of a sequence, are rows of one item: row r is token r / group, head r % group.
 #pragma once
 
+#include "decode_common.cuh"
 #include "kv8_device.cuh"
 
 namespace w4 {
 namespace kv8 {
 
 constexpr float NEG_INF = -__builtin_huge_valf();
+
+// dec::bounded_wait for barriers that hand over every microsecond or less: the
+// timer (a read of some hundred cycles) and the abort flag are looked at only
+// after many tries, so a waiter sees the phase end at once.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int* status) {
+  for (int i = 0; i < 64; ++i)
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = sm100::globaltimer_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (sm100::globaltimer_ns() - t0 > dec::WAIT_LIMIT_NS) {
+      *abort_flag = 1;
+      atomicExch(status, W4_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 struct Attn {
   const uint16_t* q;

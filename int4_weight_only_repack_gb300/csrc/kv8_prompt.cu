@@ -12,7 +12,10 @@
 // Roles (512 threads): warps 0-7 a row a thread: they scale Q to fp16, and turn S
 // into P; warps 8-11 bring in the pages and widen the e4m3 codes to fp16
 // (exactly) into the swizzled operand tiles, one layout for K (K-major) and V
-// (MN-major); warp 12 issues the products. Registers go where they are needed
+// (MN-major); warp 12 issues the products, tile 0's and tile 1's in turn (issued
+// by a warp each, the tiles fell into step and shared both the tensor cores and
+// the exponentials' units: 4770 against 3100 cycles a step). Registers go where
+// they are needed
 // (setmaxnreg 184 / 184 / 104 / 40: four times the 128 of the launch).
 //
 // The base m of a row's exponents is raised only when a score passes it by more
@@ -34,28 +37,29 @@ namespace kv8 {
 namespace {
 
 using namespace sm100;
-using dec::bounded_wait;
 using dec::drain_wait;
 
 constexpr int TILE_ROWS = 128, CTA_ROWS = 256, KT = 128, THREADS = 512, KV_STAGES = 2;
 constexpr int SOFT = 256, CONV = 128;  // threads of the roles
 constexpr int TMEM_COLS = 512;
 constexpr int BLK = 128 * 128;         // a block of 128 rows of 128 bytes (64 fp16 columns)
-constexpr int SB = KT / 16;            // sixteens of a step: each lies in one page
 constexpr int SLOTS = 4;               // steps whose scales are kept: a step's rows are done with
                                        // them when the keys three steps on are brought in
 
 struct Prompt {
   Attn a;
   int tiles;  // of the longest sequence, of CTA_ROWS rows
+  int bf16;
 };
 
-template <int D>
+// GS: tokens that share a scale, 16 or 64 (the page's, where it has that many).
+template <int D, int GS>
 struct PLayout {
+  static constexpr int SB = KT / GS;                       // groups of a step
   static constexpr int NB = D / 64;                        // 64-column blocks
   static constexpr int OFF_K = 2 * NB * BLK;               // after Q of both tiles
   static constexpr int OFF_V = OFF_K + KV_STAGES * NB * BLK;
-  static constexpr int OFF_SC = OFF_V + KV_STAGES * NB * BLK;  // [slot][SB] {ks, log2 vs, 1/vs, 0}
+  static constexpr int OFF_SC = OFF_V + KV_STAGES * NB * BLK;  // [slot][SB] {ks, log2 vs, 1/vs, -}
   static constexpr int OFF_NAN = OFF_SC + SLOTS * SB * 16;      // [slot][4] tokens with a NaN value
   static constexpr int OFF_BAR = OFF_NAN + SLOTS * 16;
   static constexpr int BARS = 4 * KV_STAGES + 8;
@@ -73,7 +77,7 @@ struct PBars {
   __device__ uint32_t pfull(int i) const { return base + 8 * (4 * KV_STAGES + 2 + i); }  // P of tile i
   __device__ uint32_t odone(int i) const { return base + 8 * (4 * KV_STAGES + 4 + i); }  // P V of tile i
   __device__ uint32_t qfull() const { return base + 8 * (4 * KV_STAGES + 6); }
-  __device__ uint32_t drained() const { return base + 8 * (4 * KV_STAGES + 7); }  // only after a timeout
+  __device__ uint32_t drained() const { return base + 8 * (4 * KV_STAGES + 7); }  // after a timeout
 };
 
 // Byte of 16-byte chunk c (of 8) of row r in a swizzled block.
@@ -113,12 +117,67 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float half_value(uint32_t h, int bf16) {
+  return bf16 ? to_float<true>((uint16_t)h) : to_float<false>((uint16_t)h);
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi, int bf16) {
+  return bf16 ? pack_out<true>(lo, hi) : pack_out<false>(lo, hi);
+}
+
+// Two fp32 values in a register pair, and arithmetic on both in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+
 // A score's factor, kept above zero: a masked score of -inf times it stays -inf.
 __device__ __forceinline__ float factor(float fr, float ks) { return fmaxf(fr * ks, 1.17549435e-38f); }
 
+// One arrival for a warp, after all its lanes' work (each lane has put its own
+// fence before it).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -128,10 +187,10 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, bool BF16>
+template <int D, int GS>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Prompt p) {
-  using L = PLayout<D>;
-  constexpr int NB = L::NB;
+  using L = PLayout<D, GS>;
+  constexpr int NB = L::NB, SB = L::SB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,17 +214,17 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 
   if (tid == 0) {
     for (int i = 0; i < KV_STAGES; ++i) {
-      mbar_init(bars.kfull(i), CONV);
-      mbar_init(bars.vfull(i), CONV);
+      mbar_init(bars.kfull(i), CONV / 32);
+      mbar_init(bars.vfull(i), CONV / 32);
       mbar_init(bars.kfree(i), 1);
       mbar_init(bars.vfree(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars.sfull(i), 1);
-      mbar_init(bars.pfull(i), SOFT / 2);
+      mbar_init(bars.pfull(i), SOFT / 64);
       mbar_init(bars.odone(i), 1);
     }
-    mbar_init(bars.qfull(), SOFT);
+    mbar_init(bars.qfull(), SOFT / 32);
     mbar_init(bars.drained(), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -213,8 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(to_float<BF16>((uint16_t)(w[k] & 0xFFFF))),
-                                   fabsf(to_float<BF16>((uint16_t)(w[k] >> 16)))));
+          amax = fmaxf(amax, fmaxf(fabsf(half_value(w[k] & 0xFFFF, p.bf16)), fabsf(half_value(w[k] >> 16, p.bf16))));
       }
       // fp16 scaled to [2^14, 2^15); a negative scale goes into Q, so that fr >= 0
       const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
@@ -227,12 +285,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         uint32_t y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          y[k] = pack_f16(to_float<BF16>((uint16_t)(w[k] & 0xFFFF)) * up,
-                          to_float<BF16>((uint16_t)(w[k] >> 16)) * up);
+          y[k] = pack_f16(half_value(w[k] & 0xFFFF, p.bf16) * up, half_value(w[k] >> 16, p.bf16) * up);
         *reinterpret_cast<uint4*>(q + (c / 8) * BLK + sw(lrow, c % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(bars.qfull());
+      warp_arrive(bars.qfull());
     }
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lanes + 128 * i, ot = tmem + lanes + 256 + D * i;
@@ -240,8 +297,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     bool ok = true;
     for (int j = 0; j < my_steps; ++j) {
       const int stage = j % KV_STAGES;
-      ok = bounded_wait(bars.kfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) &&
-           bounded_wait(bars.sfull(i), j & 1, abort_flag, a.status);
+      ok = wait_for(bars.kfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) &&
+           wait_for(bars.sfull(i), j & 1, abort_flag, a.status);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
       tc_fence_after();
@@ -267,11 +324,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       float top = NEG_INF;
 #pragma unroll
       for (int g = 0; g < SB; ++g) {
-        float y = NEG_INF;
+        float y[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y = fmaxf(y, __uint_as_float(x[g / 2][16 * (g & 1) + k]));
+        for (int k = 0; k < GS; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = GS * g + k + 2 * e;
+            y[e] = max3(y[e], x[n / 32][n % 32], x[n / 32][n % 32 + 1]);
+          }
         const float4 z = sc[g];
-        top = fmaxf(top, y * factor(fr, z.x) + z.y);
+        top = fmaxf(top, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * factor(fr, z.x) + z.y);
       }
       top -= m;
       if (__any_sync(~0u, top > room)) {
@@ -285,49 +347,53 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         const float f = first ? 0.f : ex2(-up);
         l *= f;
         if (j > 0) {
-          ok = __all_sync(~0u, bounded_wait(bars.odone(i), (j - 1) & 1, abort_flag, a.status));
+          ok = __all_sync(~0u, wait_for(bars.odone(i), (j - 1) & 1, abort_flag, a.status));
           if (!ok) break;
           tc_fence_after();
           // (before a row's first score O holds zeros, which f = 0 keeps)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t y[32];
-            tmem_ld32(ot + 32 * c, y);
+          for (int c = 0; c < D / 8; ++c) {  // (eight columns at a time: S stays in registers)
+            uint32_t y[8];
+            tmem_ld8(ot + 8 * c, y);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-            tmem_st32(ot + 32 * c, y);
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+            tmem_st8(ot + 8 * c, y);
           }
           tmem_st_wait();
         }
       }
+      uint64_t sum[SB];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t y[32];
+        uint64_t f2 = 0, add2 = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int g = 4 * c + q;
-          const float4 z = sc[g];
-          const float f = factor(fr, z.x), add = z.y - m;
-          float sum = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float s0 = __uint_as_float(x[g / 2][16 * (g & 1) + k]);
-            const float s1 = __uint_as_float(x[g / 2][16 * (g & 1) + k + 1]);
-            float p0 = ex2(s0 * f + add), p1 = ex2(s1 * f + add);
-            sum += p0 + p1;
-            y[8 * q + k / 2] = pack_f16(p0, p1);
+        for (int k = 0; k < 64; k += 2) {
+          const int n = 64 * c + k, g = n / GS;
+          if (n % GS == 0) {
+            const float4 z = sc[g];
+            const float f = factor(fr, z.x), add = z.y - m;
+            f2 = pack2(f, f);
+            add2 = pack2(add, add);
+            sum[g] = pack2(0.f, 0.f);
           }
-          l += sum * z.z;
+          const uint32_t* w = &x[n / 32][n % 32];
+          const uint64_t e = fma2(pack2(__uint_as_float(w[0]), __uint_as_float(w[1])), f2, add2);
+          const float p0 = ex2(lo2(e)), p1 = ex2(hi2(e));
+          sum[g] = add2f(sum[g], pack2(p0, p1));
+          y[k / 2] = pack_f16(p0, p1);
         }
         tmem_st32(st + 32 * c, y);
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bars.pfull(i));
+      warp_arrive(bars.pfull(i));
+#pragma unroll
+      for (int g = 0; g < SB; ++g) l += (lo2(sum[g]) + hi2(sum[g])) * sc[g].z;
     }
     if (ok && my_steps > 0)
-      ok = __all_sync(~0u, bounded_wait(bars.odone(i), (my_steps - 1) & 1, abort_flag, a.status));
+      ok = __all_sync(~0u, wait_for(bars.odone(i), (my_steps - 1) & 1, abort_flag, a.status));
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -345,8 +411,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = my_steps > 0 ? pack_out<BF16>(__uint_as_float(y[k + 2 * e]) * inv,
-                                                 __uint_as_float(y[k + 2 * e + 1]) * inv)
+            w[e] = my_steps > 0 ? pack_half(__uint_as_float(y[k + 2 * e]) * inv,
+                                            __uint_as_float(y[k + 2 * e + 1]) * inv, p.bf16)
                                 : 0u;
           *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -360,16 +426,6 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     const int32_t* table = a.table + (size_t)b * a.table_stride;
     float4* sc = reinterpret_cast<float4*>(smem + L::OFF_SC);
     uint8_t* nan = smem + L::OFF_NAN;
-    // row of the cache that holds token j (-1: none)
-    auto cache_row = [&](int j) {
-      if (j >= s.kv) return -1;
-      const int pg = table[j >> shift];
-      if ((unsigned)pg >= (unsigned)a.c.pages) {
-        record(a.status, W4_ERR_PAGE);
-        return -1;
-      }
-      return ((pg * a.c.heads + h) << shift) + (j & mask);  // below 2^31
-    };
     uint4 kr[4][NB], vr[4][NB];
     auto load = [&](uint4 (&raw)[4][NB], const uint8_t* base, const int (&at)[4]) {
 #pragma unroll
@@ -396,37 +452,49 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           *reinterpret_cast<uint4*>(to + n * BLK + sw(r, 2 * p4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
     };
-    // Codes are loaded a step ahead of their use, table entries two, scales (threads
-    // 0-7: a sixteen each) like the codes.
-    int at[4], sat = -1;
+    // Codes are loaded a step ahead of their use, table entries two (and looked at a
+    // step later, so that nothing waits for them); scales, the first
+    // threads a group each, like the codes.
+    int pg[5], at[4], sat = -1;
     float ks = 0.f, vs = 1.f;
-    auto rows_at = [&](int j) {
+    auto load_pages = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) at[i] = j < steps ? cache_row(KT * j + 32 * i + r32) : -1;
-      if (c < SB) sat = j < steps ? cache_row(KT * j + 16 * c) : -1;
+      for (int i = 0; i < 5; ++i) {
+        const int t = KT * j + (i < 4 ? 32 * i + r32 : GS * (c & (SB - 1)));
+        pg[i] = t < s.kv && j < steps ? __ldg(table + (t >> shift)) : -1;
+      }
+    };
+    auto place = [&](int i, int t) {  // the cache's row of token t (below 2^31; -1: none)
+      if (t >= s.kv) return -1;
+      if ((unsigned)pg[i] >= (unsigned)a.c.pages) {
+        record(a.status, W4_ERR_PAGE);
+        return -1;
+      }
+      return ((pg[i] * a.c.heads + h) << shift) + (t & mask);
+    };
+    auto place_all = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[i] = j < steps ? place(i, KT * j + 32 * i + r32) : -1;
+      if (c < SB) sat = j < steps ? place(4, KT * j + GS * c) : -1;
     };
     auto load_scales = [&]() {
       ks = sat < 0 ? 0.f : a.c.ks[sat >> shift];
       vs = sat < 0 ? 1.f : a.c.vs[sat >> shift];
     };
-    rows_at(0);
+    load_pages(0);
+    place_all(0);
+    load_pages(1);
     load(kr, a.c.k, at);
     load(vr, a.c.v, at);
     bool none = sat < 0;
     load_scales();
-    rows_at(1);
     for (int j = 0; j < steps; ++j) {
       const int stage = j % KV_STAGES, slot = j % SLOTS;
       const uint32_t ph = ((j / KV_STAGES) & 1) ^ 1;
-      if (!__all_sync(~0u, bounded_wait(bars.kfree(stage), ph, abort_flag, a.status))) break;
-      if (c < SB) {
-        sc[slot * SB + c] = make_float4(ks, none ? NEG_INF : __log2f(vs), __fdividef(1.f, vs), 0.f);
-        none = sat < 0;
-        load_scales();
-      }
+      if (!__all_sync(~0u, wait_for(bars.kfree(stage), ph, abort_flag, a.status))) break;
       widen(kr, smem + L::OFF_K + stage * NB * BLK);
+      if (c < SB) sc[slot * SB + c] = make_float4(ks, none ? NEG_INF : __log2f(vs), __fdividef(1.f, vs), 0.f);
       fence_proxy_async_smem();
-      load(kr, a.c.k, at);
       if (KT * j + KT > first_lim) {
         // Some row does not see every token, and 0 * NaN is NaN: NaN values leave the
         // operand and come back through the scores of the rows that see them.
@@ -451,59 +519,82 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           if (lane == 0) nan[slot * 16 + 4 * i + (warp - 8)] = (uint8_t)byte;
         }
       }
-      mbar_arrive(bars.kfull(stage));
-      if (!__all_sync(~0u, bounded_wait(bars.vfree(stage), ph, abort_flag, a.status))) break;
+      warp_arrive(bars.kfull(stage));
+      place_all(j + 1);
+      load(kr, a.c.k, at);
+      none = sat < 0;
+      if (c < SB) load_scales();
+      load_pages(j + 2);
+      if (!__all_sync(~0u, wait_for(bars.vfree(stage), ph, abort_flag, a.status))) break;
       widen(vr, smem + L::OFF_V + stage * NB * BLK);
       fence_proxy_async_smem();
-      mbar_arrive(bars.vfull(stage));
+      warp_arrive(bars.vfull(stage));
       load(vr, a.c.v, at);
-      rows_at(j + 2);
     }
   } else {
     // ------------------------------------------------------------ products
     fewer_registers<40>();
-    if (warp == 12 && lane == 0) {
+    if (__shfl_sync(~0u, warp, 0) == 12 && steps > 0) {
       constexpr uint32_t IDESC_S = idesc_f16(0, TILE_ROWS, KT);
       constexpr uint32_t IDESC_O = idesc_f16(0, TILE_ROWS, D) | (1u << 16);  // V is MN-major
-      bool ok = bounded_wait(bars.qfull(), 0, abort_flag, a.status), issued = false;
-      auto scores = [&](int i, int j) {  // S of tile i, step j
+      const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+      const uint64_t qd = smem_desc_k128(sbase);
+      const uint64_t kd = smem_desc_k128(sbase + L::OFF_K), vd = desc_v(sbase + L::OFF_V);
+      constexpr uint32_t STAGE = NB * BLK / 16;  // descriptor units of 16 bytes
+      const bool leader = elect_one();
+      bool ok = wait_for(bars.qfull(), 0, abort_flag, a.status), issued = false;
+      // S of tile i, step j (by the leader)
+      auto scores = [&](int i, int j) {
         const int stage = j % KV_STAGES;
-        if (!(ok = ok && bounded_wait(bars.kfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status))) return;
-        tc_fence_after();
-        const uint32_t qa = sbase + i * NB * BLK, ka = sbase + L::OFF_K + stage * NB * BLK;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * BLK + (k % 4) * 32;
-          umma_f16(tmem + 128 * i, smem_desc_k128(qa + off), smem_desc_k128(ka + off), IDESC_S, k != 0);
+          const uint32_t off = (k / 4) * (BLK / 16) + (k % 4) * 2;
+          umma_f16(tm + 128 * i, qd + (i * STAGE + off), kd + (stage * STAGE + off), IDESC_S, k != 0);
+        }
+      };
+      auto keys = [&](int j) { return wait_for(bars.kfull(j % KV_STAGES), (j / KV_STAGES) & 1, abort_flag, a.status); };
+      if ((ok = __all_sync(~0u, ok && keys(0)))) {
+        tc_fence_after();
+        if (leader) {
+          for (int i = 0; i < 2; ++i) {
+            if ((i ? steps1 : steps0) == 0) continue;
+            scores(i, 0);
+            umma_commit(bars.sfull(i));
+          }
+          umma_commit(bars.kfree(0));
         }
         issued = true;
-        umma_commit(bars.sfull(i));
-        // the stage is free once the last tile that uses it has read it
-        if (i == 1 || j >= steps1) umma_commit(bars.kfree(stage));
-      };
-      if (steps0 > 0) scores(0, 0);
-      if (steps1 > 0) scores(1, 0);
+      }
       for (int j = 0; ok && j < steps; ++j) {
         const int stage = j % KV_STAGES;
-        for (int i = 0; ok && i < 2; ++i) {
-          const int n = i ? steps1 : steps0;
-          if (j >= n) continue;
-          if (!(ok = bounded_wait(bars.vfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) &&
-                     bounded_wait(bars.pfull(i), j & 1, abort_flag, a.status)))
-            break;
-          tc_fence_after();
-          const uint32_t va = sbase + L::OFF_V + stage * NB * BLK;
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            umma_f16_ts(tmem + 256 + D * i, tmem + 128 * i + 8 * k, desc_v(va + k * 2048), IDESC_O,
-                        j != 0 || k != 0);
-          umma_commit(bars.odone(i));
-          if (i == 1 || j >= steps1) umma_commit(bars.vfree(stage));
-          if (j + 1 < n) scores(i, j + 1);
+        for (int i = 0; i < 2; ++i) {
+          const int n = i ? steps1 : steps0;
+          if (!ok || j >= n) continue;
+          // O += P V of this step and S of the next, one after the other with nothing
+          // waited for between: a gap there costs the tensor cores some 250 cycles
+          ok = wait_for(bars.vfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) && (j + 1 >= n || keys(j + 1)) &&
+               wait_for(bars.pfull(i), j & 1, abort_flag, a.status);
+          if (!(ok = __all_sync(~0u, ok))) continue;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+              umma_f16_ts(tm + 256 + D * i, tm + 128 * i + 8 * k, vd + (stage * STAGE + k * 128), IDESC_O,
+                          j != 0 || k != 0);
+            if (j + 1 < n) {
+              scores(i, j + 1);
+              umma_commit(bars.sfull(i));
+            }
+            umma_commit(bars.odone(i));
+            // a stage is free once the last tile that uses it has read it
+            if (i == 1 || j >= steps1) umma_commit(bars.vfree(stage));
+            if (j + 1 < n && (i == 1 || j + 1 >= steps1)) umma_commit(bars.kfree((j + 1) % KV_STAGES));
+          }
         }
       }
       if (!ok && issued) {  // let what was issued finish before the memory goes
-        umma_commit(bars.drained());
+        if (leader) umma_commit(bars.drained());
         drain_wait(bars.drained(), 0);
       }
     }
@@ -516,15 +607,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   }
 }
 
-template <int D, bool BF16>
+template <int D, int GS>
 cudaError_t launch_it(const Prompt& p, cudaStream_t s) {
   static bool done[64] = {};
-  constexpr int bytes = PLayout<D>::BYTES;
-  cudaError_t e = allow_smem(prompt_kernel<D, BF16>, bytes, done);
+  constexpr int bytes = PLayout<D, GS>::BYTES;
+  cudaError_t e = allow_smem(prompt_kernel<D, GS>, bytes, done);
   if (e != cudaSuccess) return e;
   const long long grid = (long long)p.tiles * p.a.c.heads * p.a.batch;
   if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-  return launch(prompt_kernel<D, BF16>, dim3((unsigned)grid), THREADS, bytes, s, p);
+  return launch(prompt_kernel<D, GS>, dim3((unsigned)grid), THREADS, bytes, s, p);
 }
 
 }  // namespace
@@ -532,9 +623,10 @@ cudaError_t launch_it(const Prompt& p, cudaStream_t s) {
 cudaError_t launch_prompt(const Attn& a, int dim, int bf16, cudaStream_t s) {
   Prompt p;
   p.a = a;
+  p.bf16 = bf16;
   p.tiles = (int)(((long long)a.max_q * a.group + CTA_ROWS - 1) / CTA_ROWS);
-  if (dim == 64) return bf16 ? launch_it<64, true>(p, s) : launch_it<64, false>(p, s);
-  return bf16 ? launch_it<128, true>(p, s) : launch_it<128, false>(p, s);
+  if (dim == 64) return a.c.page_shift >= 6 ? launch_it<64, 64>(p, s) : launch_it<64, 16>(p, s);
+  return a.c.page_shift >= 6 ? launch_it<128, 64>(p, s) : launch_it<128, 16>(p, s);
 }
 
 }  // namespace kv8
