@@ -453,16 +453,21 @@ def linear(x, layer: RepackedLayer, y=None, workspace=None, stream=None, bias=No
 # --------------------------------------------------------------------------- #
 # 8-bit key-value cache                                                         #
 # --------------------------------------------------------------------------- #
+# A decode step makes these calls once a layer with a few microseconds of work
+# each, so the wrappers look at every tensor once and keep what does not change.
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+_HALF_CODES = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
+
+
 class KV8Cache:
     """One layer's cache: k and v float8_e4m3fn [pages, kv_heads, page, head_dim],
     k_scale and v_scale float32 [pages, kv_heads], all contiguous on the GPU."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        if k.dim() != 4 or v.shape != k.shape or k.dtype is not torch.float8_e4m3fn or \
-                v.dtype is not torch.float8_e4m3fn:
+        if k.dim() != 4 or v.shape != k.shape or k.dtype is not _F8 or v.dtype is not _F8:
             raise ValueError("k and v must be float8_e4m3fn [pages, kv_heads, page, head_dim]")
         if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or \
-                k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+                k_scale.dtype is not _F32 or v_scale.dtype is not _F32:
             raise ValueError("k_scale and v_scale must be float32 [pages, kv_heads]")
         if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
                 and v_scale.is_contiguous()):
@@ -473,54 +478,49 @@ class KV8Cache:
                                        v_scale.data_ptr(), self.num_pages, self.page_size,
                                        self.kv_heads, self.head_dim)
         self._ref = ctypes.addressof(self._struct)
+        self._device = k.get_device()
 
 
 def kv8_cache(num_pages, kv_heads, page_size, head_dim, device="cuda") -> KV8Cache:
     """An empty cache."""
     shape = (num_pages, kv_heads, page_size, head_dim)
-    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
-            for _ in range(2))
-    ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(_F8) for _ in range(2))
+    ks, vs = (torch.ones(shape[:2], dtype=_F32, device=device) for _ in range(2))
     return KV8Cache(k, v, ks, vs)
+
+
+def _on(stream, index):
+    """The stream handle for tensors on device `index` (-1: not on a GPU)."""
+    if stream is None and index >= 0 and _RAW_STREAM is not None:
+        return _RAW_STREAM(index)
+    return _stream(stream, index if index >= 0 else None)
 
 
 def _rows(x, name, heads, dim):
     """The token stride of x [tokens, heads, dim], whose rows may be slices of a
     wider buffer but whose heads and elements are adjacent."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {tuple(shape)}")
     st = x.stride()
-    if x.shape[0] and (st[2] != 1 or (st[1] != dim and heads > 1)):
+    if shape[0] and (st[2] != 1 or (st[1] != dim and heads > 1)):
         raise ValueError(f"{name}: heads and elements of a token must be adjacent in memory")
-    return st[0] if x.shape[0] > 1 else heads * dim
+    return st[0] if shape[0] > 1 else heads * dim
 
 
 def _ints(x, name):
-    """Checks an int32 array: contiguous but for the row stride of a matrix."""
-    if x.dtype is not torch.int32 or (x.stride(-1) != 1 and x.shape[-1] > 1):
-        raise ValueError(f"{name} must be int32 with adjacent elements")
+    """The address of a contiguous int32 array."""
+    if x.dtype is not _I32 or not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32")
     return x.data_ptr()
 
 
-def _table_stride(table):
-    if table.dim() != 2:
-        raise ValueError("the table must be [sequences, pages]")
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
-
-
-def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=None):
-    """Quantises new keys and values k, v [tokens, kv_heads, head_dim] (fp16 or
-    bf16, packed by sequence: rows cu_q[b] .. cu_q[b + 1]) into the cache as each
-    sequence's last tokens: kv_lens [batch] counts them already. table [batch,
-    pages] int32 gives the sequences' pages. See w4_kv8_append in include/w4a16.h."""
-    if v.dtype is not k.dtype or v.shape != k.shape:
-        raise ValueError("k and v must have the same type and shape")
-    hk, d = cache.kv_heads, cache.head_dim
-    _check(lib().w4_kv8_append(
-        k.data_ptr(), v.data_ptr(), _rows(k, "k", hk, d), _rows(v, "v", hk, d), cache._ref,
-        _ints(table, "table"), _table_stride(table), _ints(kv_lens, "kv_lens"),
-        _ints(cu_q, "cu_q"), _batch(table, kv_lens, cu_q), k.shape[0], max_q_len,
-        dtype_code(k.dtype), _stream(stream, k.device.index)))
+def _table(x):
+    """The address and row stride of a table [sequences, pages]."""
+    st = x.stride()
+    if len(st) != 2 or x.dtype is not _I32 or (st[1] != 1 and x.shape[1] > 1):
+        raise ValueError("the table must be int32 [sequences, pages] with adjacent pages")
+    return x.data_ptr(), st[0] if x.shape[0] > 1 else x.shape[1]
 
 
 def _batch(table, kv_lens, cu_q):
@@ -530,10 +530,53 @@ def _batch(table, kv_lens, cu_q):
     return b
 
 
+def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=None):
+    """Quantises new keys and values k, v [tokens, kv_heads, head_dim] (fp16 or
+    bf16, packed by sequence: rows cu_q[b] .. cu_q[b + 1]) into the cache as each
+    sequence's last tokens: kv_lens [batch] counts them already. table [batch,
+    pages] int32 gives the sequences' pages. See w4_kv8_append in include/w4a16.h."""
+    dtype = k.dtype
+    if v.dtype is not dtype or v.shape != k.shape:
+        raise ValueError("k and v must have the same type and shape")
+    hk, d = cache.kv_heads, cache.head_dim
+    code = _HALF_CODES.get(dtype)
+    if code is None:
+        code = dtype_code(dtype)
+    tab, stride = _table(table)
+    status = lib().w4_kv8_append(
+        k.data_ptr(), v.data_ptr(), _rows(k, "k", hk, d), _rows(v, "v", hk, d), cache._ref, tab,
+        stride, _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"), _batch(table, kv_lens, cu_q),
+        k.shape[0], max_q_len, code, _on(stream, cache._device))
+    if status:
+        _check(status)
+
+
 def w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_heads, kv_heads,
                                     head_dim) -> int:
     return lib().w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_heads,
                                                  kv_heads, head_dim)
+
+
+_KV8_HEADS: dict = {}   # (q_heads, causal, scale) -> (struct, address)
+_KV8_SIZES: dict = {}   # arguments of a workspace size -> bytes
+_KV8_SPACES: dict = {}  # (device, stream) -> (tensor, address, bytes) of gemm_workspace
+_KV8_KEPT = 4096
+
+
+def _keep(kept, key, value):
+    if len(kept) >= _KV8_KEPT:
+        kept.clear()
+    kept[key] = value
+    return value
+
+
+def _space(nbytes, index, handle, stream):
+    """(address, bytes) of gemm_workspace's block for a device and stream."""
+    got = _KV8_SPACES.get((index, handle))
+    if got is None or got[2] < nbytes:
+        t = gemm_workspace(nbytes, torch.device("cuda", index), stream)
+        got = _keep(_KV8_SPACES, (index, handle), (t, t.data_ptr(), t.numel()))
+    return got[1], got[2]
 
 
 def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_len, scale=None,
@@ -543,29 +586,44 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     causal: its queries are its last tokens; otherwise each sees all of them.
     scale defaults to head_dim ** -0.5. Without `workspace`, the one kept for
     (device, stream) is used. See w4_kv8_attention in include/w4a16.h."""
-    tokens, heads, dim = q.shape
-    stride = _rows(q, "q", heads, cache.head_dim)
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
-        raise ValueError("out must be contiguous, with q's shape and type")
+    shape, dtype, dim = q.shape, q.dtype, cache.head_dim
+    tokens, heads = shape[0], shape[1]
+    stride = _rows(q, "q", heads, dim)
     batch = _batch(table, kv_lens, cu_q)
     if heads % cache.kv_heads:
         raise W4Error(2, w4_status_string(2))
-    how = _KV8HeadsStruct(heads, causal, dim ** -0.5 if scale is None else scale)
+    code = _HALF_CODES.get(dtype)
+    if code is None:
+        code = dtype_code(dtype)
+    if out is None:
+        out = q.new_empty(shape)
+    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with q's shape and type")
+    how = _KV8_HEADS.get((heads, causal, scale))
+    if how is None:
+        struct = _KV8HeadsStruct(heads, causal, dim ** -0.5 if scale is None else scale)
+        how = (struct, ctypes.addressof(struct))
+        if scale is not None:
+            _keep(_KV8_HEADS, (heads, causal, scale), how)
     L = lib()
-    nbytes = L.w4_kv8_attention_workspace_size(batch, tokens, max_q_len, max_kv_len, heads,
-                                               cache.kv_heads, dim)
+    key = (batch, tokens, max_q_len, max_kv_len, heads, cache.kv_heads, dim)
+    nbytes = _KV8_SIZES.get(key)
+    if nbytes is None:
+        nbytes = _keep(_KV8_SIZES, key, L.w4_kv8_attention_workspace_size(*key))
+    index = cache._device
+    handle = _on(stream, index)
+    space = None
     if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
+        space, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif nbytes:
-        workspace = gemm_workspace(nbytes, q.device, stream)
-    _check(L.w4_kv8_attention(
-        q.data_ptr(), stride, cache._ref, _ints(table, "table"), _table_stride(table),
-        _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len,
-        max_kv_len, ctypes.addressof(how), dtype_code(q.dtype),
-        None if workspace is None else workspace.data_ptr(), nbytes,
-        _stream(stream, q.device.index)))
+        space, nbytes = _space(nbytes, index, handle, stream)
+    tab, tab_stride = _table(table)
+    status = L.w4_kv8_attention(
+        q.data_ptr(), stride, cache._ref, tab, tab_stride, _ints(kv_lens, "kv_lens"),
+        _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len, max_kv_len, how[1], code,
+        space, nbytes, handle)
+    if status:
+        _check(status)
     return out
 
 
@@ -576,27 +634,31 @@ class KV8Pool:
     status: an int32 tensor that receives each call's W4_OK or error (a call
     that fails changes nothing); without one, errors go to w4_device_status."""
 
+    __slots__ = ("refs", "table", "lens", "page_size", "status", "_args", "_status", "_device",
+                 "_bytes")
+
     def __init__(self, refs, table, lens, page_size, status=None):
-        if table.dim() != 2 or table.shape[0] != lens.shape[0]:
+        pages, seqs = refs.shape[0], lens.shape[0]
+        tab, stride = _table(table)
+        if table.shape[0] != seqs:
             raise ValueError("table must be [sequences, pages], lens [sequences]")
         self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
         self.status = status
-        self._args = (_ints(refs, "refs"), refs.shape[0], _ints(table, "table"),
-                      _table_stride(table), _ints(lens, "lens"), lens.shape[0])
+        self._args = (_ints(refs, "refs"), pages, tab, stride, _ints(lens, "lens"), seqs)
         self._status = None if status is None else _ints(status, "status")
-
-    def _workspace(self, n, stream):
-        nbytes = lib().w4_kv8_pages_workspace_size(self.refs.shape[0], n)
-        return gemm_workspace(nbytes, self.refs.device, stream).data_ptr(), nbytes
+        self._device = refs.get_device()
+        # what any of the calls needs: at most a pair or a sequence for every slot
+        self._bytes = _KV8_SIZES.get((pages, seqs))
+        if self._bytes is None:
+            self._bytes = _keep(_KV8_SIZES, (pages, seqs), w4_kv8_pages_workspace_size(pages, seqs))
 
 
 def kv8_pool(num_pages, num_seqs, max_len, page_size, device="cuda") -> KV8Pool:
     """A pool of free pages with num_seqs empty sequences of at most max_len tokens."""
-    return KV8Pool(torch.zeros(num_pages, dtype=torch.int32, device=device),
-                   torch.full((num_seqs, -(-max_len // page_size)), -1, dtype=torch.int32,
-                              device=device),
-                   torch.zeros(num_seqs, dtype=torch.int32, device=device), page_size,
-                   torch.zeros(1, dtype=torch.int32, device=device))
+    return KV8Pool(torch.zeros(num_pages, dtype=_I32, device=device),
+                   torch.full((num_seqs, -(-max_len // page_size)), -1, dtype=_I32, device=device),
+                   torch.zeros(num_seqs, dtype=_I32, device=device), page_size,
+                   torch.zeros(1, dtype=_I32, device=device))
 
 
 def w4_kv8_pages_workspace_size(num_pages, n) -> int:
@@ -606,12 +668,14 @@ def w4_kv8_pages_workspace_size(num_pages, n) -> int:
 def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
     """Lengthens every sequence s by new_tokens[s] and gives it the pages that
     takes, the lowest free ones in order."""
-    if new_tokens.shape != pool.lens.shape:
+    if new_tokens.shape[0] != pool._args[5]:
         raise ValueError("new_tokens must have an entry for every sequence")
-    ws, nbytes = pool._workspace(pool.lens.shape[0], stream)
-    _check(lib().w4_kv8_reserve(*pool._args, _ints(new_tokens, "new_tokens"), pool.page_size,
-                                pool._status, ws, nbytes,
-                                _stream(stream, pool.refs.device.index)))
+    handle = _on(stream, pool._device)
+    status = lib().w4_kv8_reserve(*pool._args, _ints(new_tokens, "new_tokens"), pool.page_size,
+                                  pool._status,
+                                  *_space(pool._bytes, pool._device, handle, stream), handle)
+    if status:
+        _check(status)
 
 
 def kv8_fork(pool: KV8Pool, src, dst, stream=None):
@@ -621,36 +685,45 @@ def kv8_fork(pool: KV8Pool, src, dst, stream=None):
     n = src.shape[0]
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    moves = torch.empty((2, n), dtype=torch.int32, device=pool.refs.device)
-    ws, nbytes = pool._workspace(n, stream)
-    copy_src, copy_dst = moves[0], moves[1]
-    _check(lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n, pool.page_size,
-                             copy_src.data_ptr(), copy_dst.data_ptr(), pool._status, ws, nbytes,
-                             _stream(stream, pool.refs.device.index)))
+    copy_src, copy_dst = src.new_empty((2, n)).unbind()
+    handle = _on(stream, pool._device)
+    status = lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n,
+                               pool.page_size, copy_src.data_ptr(), copy_dst.data_ptr(),
+                               pool._status, *_space(pool._bytes, pool._device, handle, stream),
+                               handle)
+    if status:
+        _check(status)
     return copy_src, copy_dst
 
 
 def kv8_free(pool: KV8Pool, seqs, stream=None):
     """Ends the sequences: their pages lose a reference, their slots become empty."""
-    _check(lib().w4_kv8_free(*pool._args, _ints(seqs, "seqs"), seqs.shape[0], pool.page_size,
-                             pool._status, _stream(stream, pool.refs.device.index)))
+    status = lib().w4_kv8_free(*pool._args, _ints(seqs, "seqs"), seqs.shape[0], pool.page_size,
+                               pool._status, _on(stream, pool._device))
+    if status:
+        _check(status)
 
 
 def kv8_compact(pool: KV8Pool, stream=None):
     """Renumbers the pages in use to the front of the pool. Returns (copy_src,
     copy_dst) for kv8_copy_pages in every layer's cache (-1 after the last)."""
-    moves = torch.empty((2, pool.refs.shape[0]), dtype=torch.int32, device=pool.refs.device)
-    ws, nbytes = pool._workspace(pool.lens.shape[0], stream)
-    copy_src, copy_dst = moves[0], moves[1]
-    _check(lib().w4_kv8_compact(*pool._args[:4], pool._args[5], copy_src.data_ptr(),
-                                copy_dst.data_ptr(), ws, nbytes,
-                                _stream(stream, pool.refs.device.index)))
+    refs, pages, tab, stride, _, seqs = pool._args
+    copy_src, copy_dst = pool.refs.new_empty((2, pages)).unbind()
+    handle = _on(stream, pool._device)
+    status = lib().w4_kv8_compact(refs, pages, tab, stride, seqs, copy_src.data_ptr(),
+                                  copy_dst.data_ptr(),
+                                  *_space(pool._bytes, pool._device, handle, stream), handle)
+    if status:
+        _check(status)
     return copy_src, copy_dst
 
 
 def kv8_copy_pages(cache: KV8Cache, src, dst, stream=None):
     """Copies page src[i] to page dst[i], codes and scales (entries below 0: none)."""
-    if src.shape != dst.shape:
+    n = src.shape[0]
+    if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    _check(lib().w4_kv8_copy_pages(cache._ref, _ints(src, "src"), _ints(dst, "dst"), src.shape[0],
-                                   _stream(stream, cache.k.device.index)))
+    status = lib().w4_kv8_copy_pages(cache._ref, _ints(src, "src"), _ints(dst, "dst"), n,
+                                     _on(stream, cache._device))
+    if status:
+        _check(status)

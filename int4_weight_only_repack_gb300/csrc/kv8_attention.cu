@@ -835,20 +835,6 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const __grid_constant__ R
   }
 }
 
-// Token rows of one side of the cache: [pages * heads * page][D] bytes, a box
-// `rows` of them high.
-bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)D, ((cuuint64_t)c.pages * c.heads) << c.page_shift};
-  const cuuint64_t strides[1] = {(cuuint64_t)D};
-  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Which kernel a call runs.
 bool many_rows(int max_q, int group) { return (long long)max_q * group > 64; }
 
@@ -886,6 +872,20 @@ cudaError_t launch_d(Rows& r, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Token rows of one side of the cache: [pages * heads * page][D] bytes, a box
+// `rows` of them high.
+bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, ((cuuint64_t)c.pages * c.heads) << c.page_shift};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 size_t attention_workspace_bytes(int batch, int max_q, int max_kv, int q_heads, int kv_heads,
                                  int dim) {

@@ -53,6 +53,9 @@ struct Attn {
   int* status;
 };
 
+// A tensor map over one side's token rows, a box `rows` of them high.
+bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int rows);
+
 // The kernel for many rows (kv8_prompt.cu).
 cudaError_t launch_prompt(const Attn& a, int dim, int bf16, cudaStream_t s);
 

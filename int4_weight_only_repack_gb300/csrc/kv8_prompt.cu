@@ -10,13 +10,12 @@
 // the other's exponentials. TMEM: S / P of the tiles 0-255, O 256-511.
 //
 // Roles (512 threads): warps 0-7 a row a thread: they scale Q to fp16, and turn S
-// into P; warps 8-11 bring in the pages and widen the e4m3 codes to fp16
-// (exactly) into the swizzled operand tiles, one layout for K (K-major) and V
-// (MN-major); warp 12 issues the products, tile 0's and tile 1's in turn (issued
-// by a warp each, the tiles fell into step and shared both the tensor cores and
-// the exponentials' units: 4770 against 3100 cycles a step). Registers go where
-// they are needed
-// (setmaxnreg 184 / 184 / 104 / 40: four times the 128 of the launch).
+// into P; warp 13 brings the pages' codes in by TMA, as they are, a step ahead;
+// warps 8-11 widen them to fp16 (exactly) into the swizzled operand tiles, one
+// layout for K (K-major) and V (MN-major); warp 12 issues the products, tile 0's
+// and tile 1's in turn (issued by a warp each, the tiles fell into step and shared
+// both the tensor cores and the exponentials' units). Registers go where they are
+// needed (setmaxnreg 184 / 184 / 96 / 48: four times the 128 of the launch).
 //
 // The base m of a row's exponents is raised only when a score passes it by more
 // than 8: then its warp rescales its rows of O in tensor memory, which has to
@@ -43,12 +42,14 @@ constexpr int TILE_ROWS = 128, CTA_ROWS = 256, KT = 128, THREADS = 512, KV_STAGE
 constexpr int SOFT = 256, CONV = 128;  // threads of the roles
 constexpr int TMEM_COLS = 512;
 constexpr int BLK = 128 * 128;         // a block of 128 rows of 128 bytes (64 fp16 columns)
-constexpr int SLOTS = 4;               // steps whose scales are kept: a step's rows are done with
-                                       // them when the keys three steps on are brought in
+// Steps whose scales are kept. When a step's codes are brought in, the converters
+// have taken those of the step before, so step - 5's rows are done with theirs.
+constexpr int SLOTS = 8;
 
 struct Prompt {
   Attn a;
-  int tiles;  // of the longest sequence, of CTA_ROWS rows
+  CUtensorMap tk, tv;  // token rows [pages * heads * page][D] bytes, box of a page
+  int tiles;           // of the longest sequence, of CTA_ROWS rows
   int bf16;
 };
 
@@ -59,12 +60,16 @@ struct PLayout {
   static constexpr int NB = D / 64;                        // 64-column blocks
   static constexpr int OFF_K = 2 * NB * BLK;               // after Q of both tiles
   static constexpr int OFF_V = OFF_K + KV_STAGES * NB * BLK;
-  static constexpr int OFF_SC = OFF_V + KV_STAGES * NB * BLK;  // [slot][SB] {ks, log2 vs, 1/vs, -}
-  static constexpr int OFF_NAN = OFF_SC + SLOTS * SB * 16;      // [slot][4] tokens with a NaN value
-  static constexpr int OFF_BAR = OFF_NAN + SLOTS * 16;
-  static constexpr int BARS = 4 * KV_STAGES + 8;
+  static constexpr int RAW = KT * D;                       // a step's codes
+  static constexpr int OFF_RK = OFF_V + KV_STAGES * NB * BLK, OFF_RV = OFF_RK + RAW;
+  static constexpr int OFF_SC = OFF_RV + RAW;              // [slot][SB] {ks, log2 vs, 1/vs, -}
+  static constexpr int OFF_NAN = OFF_SC + SLOTS * SB * 16; // [slot][4] tokens with a NaN value
+  static constexpr int OFF_IN = OFF_NAN + SLOTS * 16;      // [slot] sixteens that lie in a page
+  static constexpr int OFF_BAR = OFF_IN + SLOTS * 4;
+  static constexpr int BARS = 4 * KV_STAGES + 12;
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;       // + slack to align the base
+  static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 };
 
 struct PBars {
@@ -77,44 +82,48 @@ struct PBars {
   __device__ uint32_t pfull(int i) const { return base + 8 * (4 * KV_STAGES + 2 + i); }  // P of tile i
   __device__ uint32_t odone(int i) const { return base + 8 * (4 * KV_STAGES + 4 + i); }  // P V of tile i
   __device__ uint32_t qfull() const { return base + 8 * (4 * KV_STAGES + 6); }
+  __device__ uint32_t rawfull(int v) const { return base + 8 * (4 * KV_STAGES + 8 + v); }   // codes of K, V
+  __device__ uint32_t rawfree(int v) const { return base + 8 * (4 * KV_STAGES + 10 + v); }
   __device__ uint32_t drained() const { return base + 8 * (4 * KV_STAGES + 7); }  // after a timeout
 };
 
 // Byte of 16-byte chunk c (of 8) of row r in a swizzled block.
 __device__ __forceinline__ uint32_t sw(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-// V as the B operand, MN-major: rows of tokens, 64 head columns (128 bytes) a
-// row, 8-row groups of 1024 bytes (the stride along K), 64-column blocks BLK
-// apart (the stride along N).
-__device__ __forceinline__ uint64_t desc_v(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(BLK >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-// D[tmem] (+)= A[tmem] * B[smem], fp16 operands.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// Shared-memory matrix descriptors with the 128-byte swizzle, as two words. The
+// high one is the same for all: 8-row groups of 1024 bytes, the version, the
+// swizzle. The low one has the address, in units of 16 bytes, and for V, which is
+// MN-major (rows of tokens, 64 head columns a row), the stride between its
+// 64-column blocks; 8-row groups are then the stride along K.
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_v(uint32_t saddr) { return (saddr >> 4) | ((uint32_t)(BLK >> 4) << 16); }
+
+// D[tmem] (+)= A * B[smem]^T, fp16 operands, A in shared or in tensor memory.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 
   if (tid == 0) {
     for (int i = 0; i < KV_STAGES; ++i) {
-      mbar_init(bars.kfull(i), CONV / 32);
+      mbar_init(bars.kfull(i), CONV / 32 + 1);  // and the scales
       mbar_init(bars.vfull(i), CONV / 32);
       mbar_init(bars.kfree(i), 1);
       mbar_init(bars.vfree(i), 1);
@@ -223,6 +232,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       mbar_init(bars.sfull(i), 1);
       mbar_init(bars.pfull(i), SOFT / 64);
       mbar_init(bars.odone(i), 1);
+      mbar_init(bars.rawfull(i), 1);
+      mbar_init(bars.rawfree(i), CONV / 32);
     }
     mbar_init(bars.qfull(), SOFT / 32);
     mbar_init(bars.drained(), 1);
@@ -363,34 +374,31 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           tmem_st_wait();
         }
       }
-      uint64_t sum[SB];
+      uint64_t f2 = 0, add2 = 0, sum = 0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t y[32];
-        uint64_t f2 = 0, add2 = 0;
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[16];
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          const int n = 64 * c + k, g = n / GS;
+        for (int k = 0; k < 32; k += 2) {
+          const int n = 32 * c + k, g = n / GS;
           if (n % GS == 0) {
             const float4 z = sc[g];
             const float f = factor(fr, z.x), add = z.y - m;
             f2 = pack2(f, f);
             add2 = pack2(add, add);
-            sum[g] = pack2(0.f, 0.f);
+            sum = pack2(0.f, 0.f);
           }
-          const uint32_t* w = &x[n / 32][n % 32];
-          const uint64_t e = fma2(pack2(__uint_as_float(w[0]), __uint_as_float(w[1])), f2, add2);
+          const uint64_t e = fma2(pack2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), f2, add2);
           const float p0 = ex2(lo2(e)), p1 = ex2(hi2(e));
-          sum[g] = add2f(sum[g], pack2(p0, p1));
+          sum = add2f(sum, pack2(p0, p1));
           y[k / 2] = pack_f16(p0, p1);
+          if (n % GS == GS - 2) l += (lo2(sum) + hi2(sum)) * sc[g].z;
         }
-        tmem_st32(st + 32 * c, y);
+        tmem_st16(st + 16 * c, y);
       }
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(bars.pfull(i));
-#pragma unroll
-      for (int g = 0; g < SB; ++g) l += (lo2(sum[g]) + hi2(sum[g])) * sc[g].z;
     }
     if (ok && my_steps > 0)
       ok = __all_sync(~0u, wait_for(bars.odone(i), (my_steps - 1) & 1, abort_flag, a.status));
@@ -420,22 +428,30 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ pages to operand tiles
-    fewer_registers<104>();
-    const int c = tid - SOFT, p4 = c & 3, r32 = c >> 2;  // 16-byte piece p4 (+ 4 n), row r32 (+ 32 i)
-    const int shift = a.c.page_shift, mask = (1 << shift) - 1;
-    const int32_t* table = a.table + (size_t)b * a.table_stride;
-    float4* sc = reinterpret_cast<float4*>(smem + L::OFF_SC);
-    uint8_t* nan = smem + L::OFF_NAN;
-    uint4 kr[4][NB], vr[4][NB];
-    auto load = [&](uint4 (&raw)[4][NB], const uint8_t* base, const int (&at)[4]) {
+    fewer_registers<96>();
+    // A thread takes 16-byte piece p4 (+ 4 n) of row r32 (+ 32 i). Neighbouring
+    // groups of four lanes take rows r and r ^ 5: the reads of a phase of eight
+    // lanes then differ in bit 2 of the swizzled piece, the writes in bit 0.
+    const int c = tid - SOFT, p4 = c & 3, k8 = c >> 2 & 7, cw = warp - 8;
+    const int r8 = k8 & 1 ? (k8 - 1) ^ 5 : k8, r32 = 8 * cw + r8;
+    uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::OFF_NAN);
+    const uint32_t* in = reinterpret_cast<const uint32_t*>(smem + L::OFF_IN);
+    uint4 raw[4][NB];
+    auto take = [&](int at) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-          raw[i][n] = at[i] >= 0 ? dec::ldg_x(reinterpret_cast<const uint16_t*>(base + (size_t)at[i] * D + 64 * n + 16 * p4))
-                                 : make_uint4(0, 0, 0, 0);
+        for (int n = 0; n < NB; ++n) {
+          const int r = 32 * i + r32;
+          const int off = D == 128 ? r * 128 + (((p4 + 4 * n) ^ (r & 7)) << 4) : r * 64 + ((p4 ^ (r >> 1 & 3)) << 4);
+          raw[i][n] = *reinterpret_cast<const uint4*>(smem + at + off);
+        }
     };
-    auto widen = [&](const uint4 (&raw)[4][NB], uint8_t* to) {
+    auto clear = [&](int i) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) raw[i][n] = make_uint4(0, 0, 0, 0);
+    };
+    auto widen = [&](int at) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -448,108 +464,90 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             y[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(w[k] >> 16));
           }
           const int r = 32 * i + r32;
-          *reinterpret_cast<uint4*>(to + n * BLK + sw(r, 2 * p4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(to + n * BLK + sw(r, 2 * p4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+          *reinterpret_cast<uint4*>(smem + at + n * BLK + sw(r, 2 * p4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(smem + at + n * BLK + sw(r, 2 * p4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
+      fence_proxy_async_smem();
     };
-    // Codes are loaded a step ahead of their use, table entries two (and looked at a
-    // step later, so that nothing waits for them); scales, the first
-    // threads a group each, like the codes.
-    int pg[5], at[4], sat = -1;
-    float ks = 0.f, vs = 1.f;
-    auto load_pages = [&](int j) {
+    auto nan_in = [&](int i) {  // clears the NaN codes of raw[i]; whether there were any
+      bool hit = false;
 #pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const int t = KT * j + (i < 4 ? 32 * i + r32 : GS * (c & (SB - 1)));
-        pg[i] = t < s.kv && j < steps ? __ldg(table + (t >> shift)) : -1;
+      for (int n = 0; n < NB; ++n) {
+        hit |= zero_nan_codes(raw[i][n].x);
+        hit |= zero_nan_codes(raw[i][n].y);
+        hit |= zero_nan_codes(raw[i][n].z);
+        hit |= zero_nan_codes(raw[i][n].w);
       }
+      return hit;
     };
-    auto place = [&](int i, int t) {  // the cache's row of token t (below 2^31; -1: none)
-      if (t >= s.kv) return -1;
-      if ((unsigned)pg[i] >= (unsigned)a.c.pages) {
-        record(a.status, W4_ERR_PAGE);
-        return -1;
-      }
-      return ((pg[i] * a.c.heads + h) << shift) + (t & mask);
+    // tokens of the step that are none (of a page that does not exist, or past the end)
+    auto absent = [&](int j, int slot, int i) {
+      const int r = 32 * i + r32;
+      return !(in[slot] >> (r >> 4) & 1) || KT * j + r >= s.kv;
     };
-    auto place_all = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) at[i] = j < steps ? place(i, KT * j + 32 * i + r32) : -1;
-      if (c < SB) sat = j < steps ? place(4, KT * j + GS * c) : -1;
-    };
-    auto load_scales = [&]() {
-      ks = sat < 0 ? 0.f : a.c.ks[sat >> shift];
-      vs = sat < 0 ? 1.f : a.c.vs[sat >> shift];
-    };
-    load_pages(0);
-    place_all(0);
-    load_pages(1);
-    load(kr, a.c.k, at);
-    load(vr, a.c.v, at);
-    bool none = sat < 0;
-    load_scales();
+    auto wait_warp = [&](uint32_t bar, uint32_t ph) { return __all_sync(~0u, wait_for(bar, ph, abort_flag, a.status)); };
     for (int j = 0; j < steps; ++j) {
       const int stage = j % KV_STAGES, slot = j % SLOTS;
       const uint32_t ph = ((j / KV_STAGES) & 1) ^ 1;
-      if (!__all_sync(~0u, wait_for(bars.kfree(stage), ph, abort_flag, a.status))) break;
-      widen(kr, smem + L::OFF_K + stage * NB * BLK);
-      if (c < SB) sc[slot * SB + c] = make_float4(ks, none ? NEG_INF : __log2f(vs), __fdividef(1.f, vs), 0.f);
-      fence_proxy_async_smem();
-      if (KT * j + KT > first_lim) {
+      const bool edge = KT * j + KT > first_lim;
+      if (!wait_warp(bars.rawfull(0), j & 1)) break;
+      take(L::OFF_RK);
+      const bool part = KT * j + KT > s.kv || in[slot] != 0xFFu;
+      if (part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (absent(j, slot, i)) clear(i);
+      }
+      warp_arrive(bars.rawfree(0));
+      if (!wait_warp(bars.kfree(stage), ph)) break;
+      widen(L::OFF_K + stage * NB * BLK);
+      if (edge) {
         // Some row does not see every token, and 0 * NaN is NaN: NaN values leave the
-        // operand and come back through the scores of the rows that see them.
+        // operand (below) and come back through the scores of the rows that see them,
+        // which therefore have to know them first.
+        if (!wait_warp(bars.rawfull(1), j & 1)) break;
+        take(L::OFF_RV);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          bool hit = false;
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            hit |= zero_nan_codes(vr[i][n].x);
-            hit |= zero_nan_codes(vr[i][n].y);
-            hit |= zero_nan_codes(vr[i][n].z);
-            hit |= zero_nan_codes(vr[i][n].w);
-          }
+          if (part && absent(j, slot, i)) clear(i);
           // a warp has eight tokens, four lanes each: one byte of the 32 tokens' word
-          uint32_t bits = __ballot_sync(~0u, hit);
-          bits |= bits >> 1;
-          bits |= bits >> 2;
-          bits &= 0x11111111u;
-          uint32_t byte = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) byte |= (bits >> (4 * k) & 1) << k;
-          if (lane == 0) nan[slot * 16 + 4 * i + (warp - 8)] = (uint8_t)byte;
+          uint32_t byte = __reduce_or_sync(~0u, nan_in(i) ? 1u << r8 : 0u);
+          if (lane == 0) reinterpret_cast<uint8_t*>(nan)[slot * 16 + 4 * i + cw] = (uint8_t)byte;
         }
       }
       warp_arrive(bars.kfull(stage));
-      place_all(j + 1);
-      load(kr, a.c.k, at);
-      none = sat < 0;
-      if (c < SB) load_scales();
-      load_pages(j + 2);
-      if (!__all_sync(~0u, wait_for(bars.vfree(stage), ph, abort_flag, a.status))) break;
-      widen(vr, smem + L::OFF_V + stage * NB * BLK);
-      fence_proxy_async_smem();
+      if (!wait_warp(bars.rawfull(1), j & 1)) break;
+      take(L::OFF_RV);
+      if (edge || part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (part && absent(j, slot, i)) clear(i);
+          if (edge) nan_in(i);
+        }
+      }
+      warp_arrive(bars.rawfree(1));
+      if (!wait_warp(bars.vfree(stage), ph)) break;
+      widen(L::OFF_V + stage * NB * BLK);
       warp_arrive(bars.vfull(stage));
-      load(vr, a.c.v, at);
     }
   } else {
     // ------------------------------------------------------------ products
-    fewer_registers<40>();
-    if (__shfl_sync(~0u, warp, 0) == 12 && steps > 0) {
+    fewer_registers<48>();
+    const int role = __shfl_sync(~0u, warp, 0);
+    if (role == 12 && steps > 0) {
       constexpr uint32_t IDESC_S = idesc_f16(0, TILE_ROWS, KT);
       constexpr uint32_t IDESC_O = idesc_f16(0, TILE_ROWS, D) | (1u << 16);  // V is MN-major
+      constexpr uint32_t TILE = NB * BLK / 16;  // a tile or stage, in the descriptors' units
       const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      const uint64_t qd = smem_desc_k128(sbase);
-      const uint64_t kd = smem_desc_k128(sbase + L::OFF_K), vd = desc_v(sbase + L::OFF_V);
-      constexpr uint32_t STAGE = NB * BLK / 16;  // descriptor units of 16 bytes
+      const uint32_t qd = desc_kmajor(sbase), kd = desc_kmajor(sbase + L::OFF_K), vd = desc_v(sbase + L::OFF_V);
       const bool leader = elect_one();
       bool ok = wait_for(bars.qfull(), 0, abort_flag, a.status), issued = false;
-      // S of tile i, step j (by the leader)
-      auto scores = [&](int i, int j) {
-        const int stage = j % KV_STAGES;
+      auto scores = [&](int i, int j) {  // S of tile i, step j (by the leader)
+        const uint32_t q = qd + i * TILE, k0 = kd + (j % KV_STAGES) * TILE;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k / 4) * (BLK / 16) + (k % 4) * 2;
-          umma_f16(tm + 128 * i, qd + (i * STAGE + off), kd + (stage * STAGE + off), IDESC_S, k != 0);
+          umma_ss(tm + 128 * i, q + off, k0 + off, IDESC_S, k != 0);
         }
       };
       auto keys = [&](int j) { return wait_for(bars.kfull(j % KV_STAGES), (j / KV_STAGES) & 1, abort_flag, a.status); };
@@ -567,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       }
       for (int j = 0; ok && j < steps; ++j) {
         const int stage = j % KV_STAGES;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int n = i ? steps1 : steps0;
           if (!ok || j >= n) continue;
@@ -578,10 +576,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           if (!(ok = __all_sync(~0u, ok))) continue;
           tc_fence_after();
           if (leader) {
+            const uint32_t pt = tm + 128 * i, ot = tm + 256 + D * i, v0 = vd + stage * TILE;
 #pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-              umma_f16_ts(tm + 256 + D * i, tm + 128 * i + 8 * k, vd + (stage * STAGE + k * 128), IDESC_O,
-                          j != 0 || k != 0);
+            for (int k = 0; k < KT / 16; ++k) umma_ts(ot, pt + 8 * k, v0 + k * 128, IDESC_O, j != 0 || k != 0);
             if (j + 1 < n) {
               scores(i, j + 1);
               umma_commit(bars.sfull(i));
@@ -597,6 +594,64 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         if (leader) umma_commit(bars.drained());
         drain_wait(bars.drained(), 0);
       }
+    } else if (role == 13 && steps > 0) {
+      // ---------------------------------------------------------- codes and scales
+      // Lane g < 8 has the step's sixteen g: its page's number, brought in two steps
+      // ahead; the first lane of a page its copies; the first of a group its scales,
+      // brought in a step ahead.
+      const int shift = a.c.page_shift, g = lane & 7;
+      const int32_t* table = a.table + (size_t)b * a.table_stride;
+      const bool lead = lane < 8 && ((16 * g) & ((1 << shift) - 1)) == 0;
+      const bool scales = lane < 8 && (16 * g) % GS == 0;
+      const uint32_t page_bytes = (uint32_t)D << shift;
+      auto page_at = [&](int j) {
+        const int t = KT * j + 16 * g;
+        return j < steps && t < s.kv ? table[t >> shift] : -1;
+      };
+      auto row_of = [&](int j, int pg) {  // page and head; -1: no page
+        const bool real = j < steps && KT * j + 16 * g < s.kv;
+        if (real && (unsigned)pg >= (unsigned)a.c.pages) record(a.status, W4_ERR_PAGE);
+        return real && (unsigned)pg < (unsigned)a.c.pages ? pg * a.c.heads + h : -1;
+      };
+      float4* sc = reinterpret_cast<float4*>(smem + L::OFF_SC);
+      uint32_t* in = reinterpret_cast<uint32_t*>(smem + L::OFF_IN);
+      int row = row_of(0, page_at(0)), next = page_at(1);
+      float ks = 0.f, vs = 1.f;
+      auto load_scales = [&]() {
+        if (scales && row >= 0) ks = a.c.ks[row], vs = a.c.vs[row];
+      };
+      load_scales();
+      bool ok = true;
+      int last = -1, last_v = -1;  // steps whose copies were issued
+      for (int j = 0; j < steps; ++j) {
+        const int slot = j % SLOTS;
+        const uint32_t ph = (j & 1) ^ 1;
+        const uint32_t have = __ballot_sync(~0u, lane < 8 && row >= 0);
+        const uint32_t bytes = __popc(__ballot_sync(~0u, lead && row >= 0)) * page_bytes;
+        const int y = row << shift;  // (a step begins with a page)
+        if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(0), ph, abort_flag, a.status)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bars.rawfull(0), bytes);
+        __syncwarp();
+        if (lead && row >= 0) tma_load_2d(sbase + L::OFF_RK + 16 * g * D, &p.tk, bars.rawfull(0), 0, y);
+        last = j;
+        if (scales)
+          sc[slot * SB + 16 * g / GS] =
+              row < 0 ? make_float4(0.f, NEG_INF, 1.f, 0.f) : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
+        if (lane == 0) in[slot] = have;
+        warp_arrive(bars.kfull(j % KV_STAGES));
+        if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(1), ph, abort_flag, a.status)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bars.rawfull(1), bytes);
+        __syncwarp();
+        if (lead && row >= 0) tma_load_2d(sbase + L::OFF_RV + 16 * g * D, &p.tv, bars.rawfull(1), 0, y);
+        last_v = j;
+        row = row_of(j + 1, next);
+        load_scales();
+        next = page_at(j + 2);
+      }
+      if (!ok) {  // let what was issued land before the memory goes
+        if (last >= 0) drain_wait(bars.rawfull(0), last & 1);
+        if (last_v >= 0) drain_wait(bars.rawfull(1), last_v & 1);
+      }
     }
   }
   tc_fence_before();
@@ -608,13 +663,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 }
 
 template <int D, int GS>
-cudaError_t launch_it(const Prompt& p, cudaStream_t s) {
+cudaError_t launch_it(Prompt& p, cudaStream_t s) {
   static bool done[64] = {};
   constexpr int bytes = PLayout<D, GS>::BYTES;
   cudaError_t e = allow_smem(prompt_kernel<D, GS>, bytes, done);
   if (e != cudaSuccess) return e;
   const long long grid = (long long)p.tiles * p.a.c.heads * p.a.batch;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (grid >= (1ll << 31) || !encode_rows(&p.tk, p.a.c.k, p.a.c, D, 1 << p.a.c.page_shift) ||
+      !encode_rows(&p.tv, p.a.c.v, p.a.c, D, 1 << p.a.c.page_shift))
+    return cudaErrorInvalidValue;
   return launch(prompt_kernel<D, GS>, dim3((unsigned)grid), THREADS, bytes, s, p);
 }
 
