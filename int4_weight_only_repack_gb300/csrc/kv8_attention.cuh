@@ -27,14 +27,16 @@ constexpr float NEG_INF = -__builtin_huge_valf();
 // after many tries, so a waiter sees the phase end at once.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
-  for (int i = 0; i < 64; ++i)
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = sm100::globaltimer_ns();
+  if (__builtin_expect(sm100::mbar_try_wait(bar, parity), 1)) return true;
+  uint64_t t0 = 0;
   for (;;) {
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (sm100::mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (sm100::globaltimer_ns() - t0 > dec::WAIT_LIMIT_NS) {
+    const uint64_t t = sm100::globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > dec::WAIT_LIMIT_NS) {
       *abort_flag = 1;
       atomicExch(status, W4_ERR_TIMEOUT);
       return false;

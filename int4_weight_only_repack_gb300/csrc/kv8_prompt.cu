@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         }
         issued = true;
       }
+      int seen = -1;
       for (int j = 0; ok && j < steps; ++j) {
         const int stage = j % KV_STAGES;
 #pragma unroll 1
@@ -571,8 +572,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           if (!ok || j >= n) continue;
           // O += P V of this step and S of the next, one after the other with nothing
           // waited for between: a gap there costs the tensor cores some 250 cycles
-          ok = wait_for(bars.vfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) && (j + 1 >= n || keys(j + 1)) &&
-               wait_for(bars.pfull(i), j & 1, abort_flag, a.status);
+          // (the keys of a step are announced after the values of the one before)
+          if (j != seen) {
+            ok = j + 1 < steps ? keys(j + 1) : wait_for(bars.vfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status);
+            seen = j;
+          }
+          ok = ok && wait_for(bars.pfull(i), j & 1, abort_flag, a.status);
           if (!(ok = __all_sync(~0u, ok))) continue;
           tc_fence_after();
           if (leader) {
