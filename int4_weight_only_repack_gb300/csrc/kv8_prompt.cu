@@ -635,14 +635,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         const uint32_t bytes = __popc(__ballot_sync(~0u, lead && row >= 0)) * page_bytes;
         const int y = row << shift;  // (a step begins with a page)
         if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(0), ph, abort_flag, a.status)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(bars.rawfull(0), bytes);
+        if (lane == 0) {  // (what the converters read of the step comes before its barrier)
+          in[slot] = have;
+          mbar_arrive_expect_tx(bars.rawfull(0), bytes);
+        }
         __syncwarp();
         if (lead && row >= 0) tma_load_2d(sbase + L::OFF_RK + 16 * g * D, &p.tk, bars.rawfull(0), 0, y);
         last = j;
         if (scales)
           sc[slot * SB + 16 * g / GS] =
               row < 0 ? make_float4(0.f, NEG_INF, 1.f, 0.f) : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
-        if (lane == 0) in[slot] = have;
         warp_arrive(bars.kfull(j % KV_STAGES));
         if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(1), ph, abort_flag, a.status)))) break;
         if (lane == 0) mbar_arrive_expect_tx(bars.rawfull(1), bytes);
