@@ -71,11 +71,7 @@ __global__ void __launch_bounds__(AT) append_kernel(const Append a) {
   const int pi = (first >> shift) + idx;         // page of the sequence
   const int lo = max(first, pi << shift), hi = min(kv, (pi + 1) << shift);
   if (lo >= hi) return;
-  const int p = a.table[(size_t)b * a.table_stride + pi];
-  if (p < 0 || p >= a.c.pages) {
-    if (threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
-    return;
-  }
+  const int p = a.table[(size_t)b * a.table_stride + pi];  // (looked at after the elements are on their way)
   constexpr int RP = D / 8;  // 16-byte pieces of a row
   const int pieces = (hi - lo) * RP;
   const size_t stride = is_v ? a.v_stride : a.k_stride;
@@ -88,6 +84,14 @@ __global__ void __launch_bounds__(AT) append_kernel(const Append a) {
     if (i < pieces)
       x[j] = *reinterpret_cast<const uint4*>(src + (size_t)(i / RP) * stride + (i % RP) * 8);
   }
+  if (p < 0 || p >= a.c.pages) {
+    if (threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
+    return;
+  }
+  const size_t ph = (size_t)p * a.c.heads + h;
+  float* scale = (is_v ? a.c.vs : a.c.ks) + ph;
+  const int held = lo - (pi << shift);  // this sequence's tokens already in the page
+  const float old = held > 0 ? *scale : 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     if (threadIdx.x + j * AT < pieces) {
@@ -103,10 +107,6 @@ __global__ void __launch_bounds__(AT) append_kernel(const Append a) {
   for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
   __shared__ float red[AT / 32];
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  const size_t ph = (size_t)p * a.c.heads + h;
-  float* scale = (is_v ? a.c.vs : a.c.ks) + ph;
-  const int held = lo - (pi << shift);  // this sequence's tokens already in the page
-  const float old = held > 0 ? *scale : 0.f;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < AT / 32; ++i) amax = fmaxf(amax, red[i]);
