@@ -596,7 +596,7 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     if code is None:
         code = dtype_code(dtype)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with q's shape and type")
     how = _KV8_HEADS.get((heads, causal, scale))
@@ -685,7 +685,7 @@ def kv8_fork(pool: KV8Pool, src, dst, stream=None):
     n = src.shape[0]
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
-    copy_src, copy_dst = src.new_empty((2, n)).unbind()
+    copy_src, copy_dst = torch.empty((2, n), dtype=_I32, device=src.device).unbind()
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n,
                                pool.page_size, copy_src.data_ptr(), copy_dst.data_ptr(),
@@ -708,7 +708,7 @@ def kv8_compact(pool: KV8Pool, stream=None):
     """Renumbers the pages in use to the front of the pool. Returns (copy_src,
     copy_dst) for kv8_copy_pages in every layer's cache (-1 after the last)."""
     refs, pages, tab, stride, _, seqs = pool._args
-    copy_src, copy_dst = pool.refs.new_empty((2, pages)).unbind()
+    copy_src, copy_dst = torch.empty((2, pages), dtype=_I32, device=pool.refs.device).unbind()
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_compact(refs, pages, tab, stride, seqs, copy_src.data_ptr(),
                                   copy_dst.data_ptr(),
