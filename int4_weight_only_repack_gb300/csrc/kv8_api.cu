@@ -153,8 +153,8 @@ w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_stride, s
 size_t w4_kv8_attention_workspace_size(int batch, int total_q, int max_q_len, int max_kv_len,
                                        int q_heads, int kv_heads, int head_dim) {
   if (batch < 1 || batch > MAX_BATCH || total_q < 1 || total_q > MAX_TOKENS || max_q_len < 1 ||
-      max_q_len > MAX_TOKENS || max_kv_len < 0 || q_heads < 1 || q_heads > MAX_HEADS ||
-      kv_heads < 1 || q_heads % kv_heads || (head_dim != 64 && head_dim != 128))
+      max_q_len > MAX_TOKENS || max_kv_len < 0 || max_kv_len > MAX_KV || q_heads < 1 ||
+      q_heads > MAX_HEADS || kv_heads < 1 || q_heads % kv_heads || (head_dim != 64 && head_dim != 128))
     return 0;
   return attention_workspace_bytes(batch, max_q_len, max_kv_len, q_heads, kv_heads, head_dim);
 }
@@ -171,7 +171,7 @@ w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_cache* c
   if ((st = check_batch(table, table_stride, kv_lens, cu_q, batch, total_q, max_q_len, dtype)))
     return st;
   if (q_heads < 1 || q_heads > MAX_HEADS || q_heads % cache->kv_heads || max_kv_len < 0 ||
-      heads->causal < 0 || heads->causal > 1 || !std::isfinite(heads->scale))
+      max_kv_len > MAX_KV || heads->causal < 0 || heads->causal > 1 || !std::isfinite(heads->scale))
     return W4_ERR_SHAPE;
   const int width = q_heads * cache->head_dim;
   if (bad_stride(q_stride, width)) return W4_ERR_SHAPE;

@@ -9,8 +9,9 @@
 // kernel joins them (in the order of the tokens, so the result does not depend
 // on timing). Joining in the first kernel, by whoever finishes an item's last
 // part, measured 14 to 20 us a call, all of it on the critical path: the write,
-// the fence, the count and the reads wait for one another. Where no sequence is longer than 512 tokens every item gets a CTA of its own, whose
-// warps take units in turn and are joined in shared memory, and that is all.
+// the fence, the count and the reads wait for one another. Where no sequence is
+// longer than 512 tokens every item gets a CTA of its own, whose warps take units
+// in turn and are joined in shared memory, and that is all.
 //
 // Each warp brings its units in by TMA through a ring of its own (keys and
 // values, 128-byte swizzle, so that the 16-byte shared loads below are free of
@@ -40,7 +41,9 @@ constexpr int WARPS = 4, THREADS = WARPS * 32, STEP = 32, STAGES = 2;
 constexpr int MAX_SMS = 160;       // that a split call uses
 constexpr int MAX_SCAN = 2048;     // sequences of a split call: every CTA scans their lengths
 constexpr int ITEM_TOKENS = 512;   // sequences up to this long are not split
-constexpr int MIN_COST = 6;        // of a warp's run in a split call
+// Of a warp's run in a split call. 16 tokens on 2048 to 8192 cached ones, group of
+// 4: 17.1 us with 3 and 4, 18.2 with 6, 21.6 with 10, 26.2 with 16.
+constexpr int MIN_COST = 4;
 // Two CTAs an SM keep 128 KB of copies in flight. Three (168 registers) measured
 // slower: 51.3 against 42.1 us on 64 ragged sequences of up to 4096 tokens, 102.5
 // against 95.9 us on two of 131072, whose warps then end further apart.
@@ -889,7 +892,9 @@ bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int 
 
 size_t attention_workspace_bytes(int batch, int max_q, int max_kv, int q_heads, int kv_heads,
                                  int dim) {
-  if (many_rows(max_q, q_heads / kv_heads) || !splits(batch, max_kv)) return 0;
+  if (many_rows(max_q, q_heads / kv_heads))
+    return prompt_workspace_bytes(batch, max_q, max_kv, q_heads / kv_heads, kv_heads, dim);
+  if (!splits(batch, max_kv)) return 0;
   const int nb = row_blocks((long long)max_q * (q_heads / kv_heads));
   return (size_t)MAX_WORKERS * sizeof(Begun) + (size_t)MAX_WORKERS * 2 * part_floats(dim, nb) * 4;
 }
@@ -904,7 +909,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s) {
   r.a = {a.q, a.q_stride, a.c, a.table, a.kv_lens, a.cu_q, a.out, a.table_stride, a.batch,
          a.total_q, a.max_q, a.max_kv, a.q_heads, a.q_heads / a.c.heads, a.causal,
          a.scale * 1.44269504088896340736f, status};
-  if (many_rows(a.max_q, r.a.group)) return launch_prompt(r.a, a.dim, a.bf16, s);
+  if (many_rows(a.max_q, r.a.group)) return launch_prompt(r.a, a.dim, a.bf16, a.workspace, s);
   const int box = std::min(1 << a.c.page_shift, STEP);
   if (!encode_rows(&r.tk, a.c.k, a.c, a.dim, box) || !encode_rows(&r.tv, a.c.v, a.c, a.dim, box))
     return cudaErrorInvalidValue;

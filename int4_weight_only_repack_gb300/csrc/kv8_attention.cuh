@@ -59,7 +59,8 @@ struct Attn {
 bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int rows);
 
 // The kernel for many rows (kv8_prompt.cu).
-cudaError_t launch_prompt(const Attn& a, int dim, int bf16, cudaStream_t s);
+cudaError_t launch_prompt(const Attn& a, int dim, int bf16, void* workspace, cudaStream_t s);
+size_t prompt_workspace_bytes(int batch, int max_q, int max_kv, int group, int kv_heads, int dim);
 
 template <bool BF16>
 __device__ __forceinline__ float to_float(uint16_t h) {

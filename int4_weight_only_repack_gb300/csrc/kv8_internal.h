@@ -11,6 +11,7 @@ namespace kv8 {
 
 constexpr int MAX_BATCH = 1 << 20;
 constexpr int MAX_TOKENS = 1 << 24;  // new tokens of a call
+constexpr int MAX_KV = 1 << 30;      // tokens that a sequence holds
 constexpr int MAX_HEADS = 1024;
 
 // What the kernels need of a cache: pages as rows of head_dim bytes.

@@ -468,3 +468,28 @@ def test_workspace_contents_do_not_matter(w4):
         got = w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds([1] * 5), 1, 5000,
                                workspace=ws)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,n,m,page,causal", [
+    (8, 1, 128, 5000, 60, 64, True), (16, 2, 64, 3001, 40, 16, True), (9, 1, 64, 2000, 131, 128, False),
+    (70, 1, 128, 2500, 1, 32, True), (4, 1, 128, 300, 300, 64, True)])
+def test_few_tiles_over_a_long_axis(w4, heads, kv_heads, dim, n, m, page, causal):
+    """Few tiles of many rows: their steps are split over thread blocks and joined.
+    One sequence is short, so that some parts of it are empty; one has no token."""
+    lens, counts = [n, 130, 0], [m, min(m, 130), 2]
+    pages = 2 * (n // page + 3)
+    cache = ref.random_cache(w4, pages, kv_heads, page, dim, seed=70, scales="any")
+    table = ref.scattered_table(lens, page, pages, seed=71)
+    q = queries(sum(counts), heads, dim, "bf16", 72)
+    check(w4, q, cache, table, lens, counts, causal, "bf16")
+    need = w4.w4_kv8_attention_workspace_size(3, sum(counts), m, n, heads, kv_heads, dim)
+    assert (need > 0) == (n > 15 * 128)
+
+
+def test_several_items_for_every_sm(w4):
+    """More tiles than the GPU holds at once, of one and of two halves."""
+    n, heads, kv_heads, dim, page = 300, 320, 160, 64, 64
+    cache = ref.random_cache(w4, 8, kv_heads, page, dim, seed=73)
+    table = ref.scattered_table([n], page, 8, seed=74)
+    q = queries(n, heads, dim, "fp16", 75)
+    check(w4, q, cache, table, [n], [n], True, "fp16")

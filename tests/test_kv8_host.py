@@ -170,3 +170,10 @@ def test_binding_refusals(w4):
         w4.kv8_append(x[:, :2], x[:, :2].half(), c, t, n, cu, 1)
     with pytest.raises(ValueError):
         w4.KV8Pool(n, t, torch.zeros(3, dtype=torch.int32), 16)
+
+
+def test_tokens_past_every_cache(w4):
+    """Token positions, rounded up to a tile, have to stay inside 32 bits."""
+    c = cache(w4)
+    assert attend(w4, c, kv=(1 << 30) + 1) == SHAPE
+    assert w4.w4_kv8_attention_workspace_size(2, 2, 1, (1 << 30) + 1, 32, 8, 128) == 0
