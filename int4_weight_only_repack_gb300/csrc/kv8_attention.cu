@@ -41,8 +41,8 @@ constexpr int WARPS = 4, THREADS = WARPS * 32, STEP = 32, STAGES = 2;
 constexpr int MAX_SMS = 160;       // that a split call uses
 constexpr int MAX_SCAN = 2048;     // sequences of a split call: every CTA scans their lengths
 constexpr int ITEM_TOKENS = 512;   // sequences up to this long are not split
-// Of a warp's run in a split call. 16 tokens on 2048 to 8192 cached ones, group of
-// 4: 17.1 us with 3 and 4, 18.2 with 6, 21.6 with 10, 26.2 with 16.
+// Of a warp's run in a split call. 24 sequences of 35 to 3001 tokens, 1 to 6 new,
+// groups of 7: 17.1 us with 3 and 4, 18.2 with 6, 21.6 with 10, 26.2 with 16.
 constexpr int MIN_COST = 4;
 // Two CTAs an SM keep 128 KB of copies in flight. Three (168 registers) measured
 // slower: 51.3 against 42.1 us on 64 ragged sequences of up to 4096 tokens, 102.5
