@@ -25,6 +25,16 @@
 // items as SMs, an item's steps are dealt to several CTAs, whose sums a second
 // kernel joins.
 //
+// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 419 us,
+// 1250 TFLOP/s, 65 % of the cuBLAS rate. A step takes about 3250 cycles where its
+// products alone are 2048, and a CTA about 9 us beyond its steps (its first codes
+// and queries, the first step, the output). Neither the exponentials nor the
+// widening is what a step waits for: without the first it took 399 us, without the
+// second 414. It is the chain S, tensor memory to registers and back, P V of a
+// tile, which tensor memory (full with two tiles) does not let overlap itself.
+// Taking the exponentials before the row's largest is known, and again in the rare
+// step that raises the base, measured the same (423 us).
+//
 // The base m of a row's exponents is raised only when a score passes it by more
 // than 8: then its warp rescales its rows of O in tensor memory, which has to
 // wait for the tile's last product; otherwise it never touches O.
