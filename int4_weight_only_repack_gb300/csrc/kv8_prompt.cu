@@ -25,15 +25,16 @@
 // items as SMs, an item's steps are dealt to several CTAs, whose sums a second
 // kernel joins.
 //
-// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 419 us,
-// 1250 TFLOP/s, 65 % of the cuBLAS rate. A step takes about 3250 cycles where its
+// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 416 us,
+// 1260 TFLOP/s, 66 % of the cuBLAS rate. A step takes about 3250 cycles where its
 // products alone are 2048, and a CTA about 9 us beyond its steps (its first codes
-// and queries, the first step, the output). Neither the exponentials nor the
+// and queries, the first step, the output; its first page numbers and scales are
+// read before the barriers are set up, which is worth 2 to 6 us a call). Neither the exponentials nor the
 // widening is what a step waits for: without the first it took 399 us, without the
-// second 414. It is the chain S, tensor memory to registers and back, P V of a
+// second 414 (of 419 then). It is the chain S, tensor memory to registers and back, P V of a
 // tile, which tensor memory (full with two tiles) does not let overlap itself.
 // Taking the exponentials before the row's largest is known, and again in the rare
-// step that raises the base, measured the same (423 us).
+// step that raises the base, measured the same (423 us of 419).
 //
 // The base m of a row's exponents is raised only when a score passes it by more
 // than 8: then its warp rescales its rows of O in tensor memory, which has to
@@ -245,6 +246,48 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   const int rows = s.n * a.group, row0 = tile * CTA_ROWS;
   if (row0 >= rows) return;
 
+  // tokens that a tile's last row sees, and its steps (tile 1 has the later rows)
+  auto tokens_of = [&](int i) {
+    const int first = row0 + TILE_ROWS * i;
+    if (first >= rows) return 0;
+    const int tok = (min(rows, first + TILE_ROWS) - 1) / a.group;
+    return a.causal ? max(0, min(s.kv, s.kv - s.n + tok + 1)) : s.kv;
+  };
+  // this part's: steps0 and steps1 of them from token k0 on
+  const int all0 = (tokens_of(0) + KT - 1) / KT, all1 = (tokens_of(1) + KT - 1) / KT;
+  const int per = (max(all0, all1) + parts - 1) / parts, j0 = part * per, k0 = KT * j0;
+  const int steps0 = max(0, min(all0 - j0, per)), steps1 = max(0, min(all1 - j0, per));
+  const int steps = max(steps0, steps1);
+  // tokens from which on some row of the CTA does not see all
+  const int first_lim = a.causal ? max(0, min(s.kv, s.kv - s.n + row0 / a.group + 1)) : s.kv;
+
+  // For the warp that brings codes in: lane g < 8 has the step's sixteen g, its page's
+  // number, read two steps ahead; the first lane of a page has its copies, the first
+  // of a group its scales, read a step ahead.
+  const int shift = a.c.page_shift, g = lane & 7;
+  const int32_t* table = a.table + (size_t)b * a.table_stride;
+  const bool lead = lane < 8 && ((16 * g) & ((1 << shift) - 1)) == 0;
+  const bool scales = lane < 8 && (16 * g) % GS == 0;
+  const uint32_t page_bytes = (uint32_t)D << shift;
+  auto page_at = [&](int j) {
+    const int t = k0 + KT * j + 16 * g;
+    return j < steps && t < s.kv ? table[t >> shift] : -1;
+  };
+  auto row_of = [&](int j, int pg) {  // page and head; -1: no page
+    const bool real = j < steps && k0 + KT * j + 16 * g < s.kv;
+    if (real && (unsigned)pg >= (unsigned)a.c.pages) record(a.status, W4_ERR_PAGE);
+    return real && (unsigned)pg < (unsigned)a.c.pages ? pg * a.c.heads + h : -1;
+  };
+  int page_row = -1, next = -1;
+  float ks = 0.f, vs = 1.f;
+  auto load_scales = [&]() {
+    if (scales && page_row >= 0) ks = a.c.ks[page_row], vs = a.c.vs[page_row];
+  };
+  if (warp == 13) {  // (on their way before the barriers are ready)
+    page_row = row_of(0, page_at(0)), next = page_at(1);
+    load_scales();
+  }
+
   if (tid == 0) {
     for (int i = 0; i < KV_STAGES; ++i) {
       mbar_init(bars.kfull(i), CONV / 32 + 1);  // and the scales
@@ -272,21 +315,6 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-
-  // tokens that a tile's last row sees, and its steps (tile 1 has the later rows)
-  auto tokens_of = [&](int i) {
-    const int first = row0 + TILE_ROWS * i;
-    if (first >= rows) return 0;
-    const int tok = (min(rows, first + TILE_ROWS) - 1) / a.group;
-    return a.causal ? max(0, min(s.kv, s.kv - s.n + tok + 1)) : s.kv;
-  };
-  // this part's: steps0 and steps1 of them from token k0 on
-  const int all0 = (tokens_of(0) + KT - 1) / KT, all1 = (tokens_of(1) + KT - 1) / KT;
-  const int per = (max(all0, all1) + parts - 1) / parts, j0 = part * per, k0 = KT * j0;
-  const int steps0 = max(0, min(all0 - j0, per)), steps1 = max(0, min(all1 - j0, per));
-  const int steps = max(steps0, steps1);
-  // tokens from which on some row of the CTA does not see all
-  const int first_lim = a.causal ? max(0, min(s.kv, s.kv - s.n + row0 / a.group + 1)) : s.kv;
 
   if (warp < 8) {
     // ------------------------------------------------------------ rows: Q, then S to P
@@ -638,57 +666,35 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       }
     } else if (role == 13 && steps > 0) {
       // ---------------------------------------------------------- codes and scales
-      // Lane g < 8 has the step's sixteen g: its page's number, brought in two steps
-      // ahead; the first lane of a page its copies; the first of a group its scales,
-      // brought in a step ahead.
-      const int shift = a.c.page_shift, g = lane & 7;
-      const int32_t* table = a.table + (size_t)b * a.table_stride;
-      const bool lead = lane < 8 && ((16 * g) & ((1 << shift) - 1)) == 0;
-      const bool scales = lane < 8 && (16 * g) % GS == 0;
-      const uint32_t page_bytes = (uint32_t)D << shift;
-      auto page_at = [&](int j) {
-        const int t = k0 + KT * j + 16 * g;
-        return j < steps && t < s.kv ? table[t >> shift] : -1;
-      };
-      auto row_of = [&](int j, int pg) {  // page and head; -1: no page
-        const bool real = j < steps && k0 + KT * j + 16 * g < s.kv;
-        if (real && (unsigned)pg >= (unsigned)a.c.pages) record(a.status, W4_ERR_PAGE);
-        return real && (unsigned)pg < (unsigned)a.c.pages ? pg * a.c.heads + h : -1;
-      };
       float4* sc = reinterpret_cast<float4*>(smem + L::OFF_SC);
       uint32_t* in = reinterpret_cast<uint32_t*>(smem + L::OFF_IN);
-      int row = row_of(0, page_at(0)), next = page_at(1);
-      float ks = 0.f, vs = 1.f;
-      auto load_scales = [&]() {
-        if (scales && row >= 0) ks = a.c.ks[row], vs = a.c.vs[row];
-      };
-      load_scales();
       bool ok = true;
       int last = -1, last_v = -1;  // steps whose copies were issued
       for (int j = 0; j < steps; ++j) {
         const int slot = j % SLOTS;
         const uint32_t ph = (j & 1) ^ 1;
-        const uint32_t have = __ballot_sync(~0u, lane < 8 && row >= 0);
-        const uint32_t bytes = __popc(__ballot_sync(~0u, lead && row >= 0)) * page_bytes;
-        const int y = row << shift;  // (a step begins with a page)
+        const uint32_t have = __ballot_sync(~0u, lane < 8 && page_row >= 0);
+        const uint32_t bytes = __popc(__ballot_sync(~0u, lead && page_row >= 0)) * page_bytes;
+        const int y = page_row << shift;  // (a step begins with a page)
         if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(0), ph, abort_flag, a.status)))) break;
         if (lane == 0) {  // (what the converters read of the step comes before its barrier)
           in[slot] = have;
           mbar_arrive_expect_tx(bars.rawfull(0), bytes);
         }
         __syncwarp();
-        if (lead && row >= 0) tma_load_2d(sbase + L::OFF_RK + 16 * g * D, &p.tk, bars.rawfull(0), 0, y);
+        if (lead && page_row >= 0) tma_load_2d(sbase + L::OFF_RK + 16 * g * D, &p.tk, bars.rawfull(0), 0, y);
         last = j;
         if (scales)
           sc[slot * SB + 16 * g / GS] =
-              row < 0 ? make_float4(0.f, NEG_INF, 1.f, 0.f) : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
+              page_row < 0 ? make_float4(0.f, NEG_INF, 1.f, 0.f)
+                           : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
         warp_arrive(bars.kfull(j % KV_STAGES));
         if (!(ok = __all_sync(~0u, wait_for(bars.rawfree(1), ph, abort_flag, a.status)))) break;
         if (lane == 0) mbar_arrive_expect_tx(bars.rawfull(1), bytes);
         __syncwarp();
-        if (lead && row >= 0) tma_load_2d(sbase + L::OFF_RV + 16 * g * D, &p.tv, bars.rawfull(1), 0, y);
+        if (lead && page_row >= 0) tma_load_2d(sbase + L::OFF_RV + 16 * g * D, &p.tv, bars.rawfull(1), 0, y);
         last_v = j;
-        row = row_of(j + 1, next);
+        page_row = row_of(j + 1, next);
         load_scales();
         next = page_at(j + 2);
       }
