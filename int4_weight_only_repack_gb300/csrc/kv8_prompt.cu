@@ -28,13 +28,13 @@
 // Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 416 us,
 // 1260 TFLOP/s, 66 % of the cuBLAS rate. A step takes about 3250 cycles where its
 // products alone are 2048, and a CTA about 9 us beyond its steps (its first codes
-// and queries, the first step, the output; its first page numbers and scales are
-// read before the barriers are set up, which is worth 2 to 6 us a call). Neither the exponentials nor the
-// widening is what a step waits for: without the first it took 399 us, without the
-// second 414 (of 419 then). It is the chain S, tensor memory to registers and back, P V of a
-// tile, which tensor memory (full with two tiles) does not let overlap itself.
-// Taking the exponentials before the row's largest is known, and again in the rare
-// step that raises the base, measured the same (423 us of 419).
+// and queries, the first step, the output; reading its first page numbers and
+// scales before the barriers are set up is worth 2 to 6 us a call). Neither the
+// exponentials nor the widening is what a step waits for: of 419 us, a build without
+// the first took 399, one without the second 414. It is the chain of a tile: S, from
+// tensor memory to registers and back, P V, which tensor memory (full with two
+// tiles) does not let overlap itself. Taking the exponentials before the row's
+// largest is known, and again in the rare step that raises the base, took 423 us.
 //
 // The base m of a row's exponents is raised only when a score passes it by more
 // than 8: then its warp rescales its rows of O in tensor memory, which has to
