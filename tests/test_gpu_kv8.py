@@ -493,3 +493,58 @@ def test_several_items_for_every_sm(w4):
     table = ref.scattered_table([n], page, 8, seed=74)
     q = queries(n, heads, dim, "fp16", 75)
     check(w4, q, cache, table, [n], [n], True, "fp16")
+
+
+def split_case(w4, seed, dim=128, page=64, n=2900, m=50):
+    """A call whose tiles are split along the tokens, and a workspace of its size."""
+    lens, counts = [n, 2100], [m, 7]
+    cache = ref.random_cache(w4, 2 * (n // page + 1), 1, page, dim, seed=seed, scales="any")
+    table = ref.scattered_table(lens, page, cache.num_pages, seed=seed + 1)
+    q = queries(sum(counts), 8, dim, "fp16", seed + 2)
+    size = w4.w4_kv8_attention_workspace_size(2, sum(counts), m, n, 8, 1, dim)
+    assert size > 0
+    return lens, counts, cache, table, q, size
+
+
+def test_split_tiles_workspace_contents_do_not_matter(w4):
+    lens, counts, cache, table, q, size = split_case(w4, 80)
+    want = check(w4, q, cache, table, lens, counts, True, "fp16")
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got = w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds(counts), max(counts),
+                               max(lens), workspace=ws)
+        assert torch.equal(got, want)
+    with pytest.raises(w4.W4Error):
+        w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds(counts), max(counts),
+                         max(lens), workspace=ws[:size - 1])
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_split_tiles_nan_reaches_only_rows_that_see_it(w4, page):
+    """In the last tokens, where rows differ in what they see, and in the first."""
+    m, n = 50, 2900
+    lens, counts, cache, table, q, _ = split_case(w4, 90, page=page, n=n, m=m)
+    args = (cache, table, ref.ints(lens), ref.bounds(counts), m, n)
+    clean = w4.kv8_attention(q, *args)
+    for spot in (n - 1 - m // 2, 3):
+        for codes in (cache.k, cache.v):
+            raw = codes.view(torch.uint8)
+            at = (table[0, spot // page].long(), 0, spot % page, 5)
+            keep = raw[at].clone()
+            raw[at] = 0x7F
+            got = w4.kv8_attention(q, *args)
+            raw[at] = keep
+            sees = torch.arange(sum(counts), device="cuda") >= spot - (n - m)
+            sees[m:] = False  # the other sequence
+            assert torch.equal(got[~sees], clean[~sees])
+            assert torch.isnan(got[sees]).any(-1).all()
+
+
+def test_split_tiles_extreme_scores(w4):
+    """The parts' bases differ by thousands, their value scales by 2^60."""
+    lens, counts, cache, table, q, _ = split_case(w4, 100, page=16)
+    cache.v_scale.copy_(torch.exp2(torch.linspace(-40, 20, cache.num_pages, device="cuda").round())[:, None])
+    for mag in (1e-6, 1.0, 300.0):
+        check(w4, (q.float() * mag).half(), cache, table, lens, counts, False, "fp16",
+              scale=1.0 if mag > 1 else 0.1)
+    check(w4, torch.zeros_like(q), cache, table, lens, counts, True, "fp16")
