@@ -508,6 +508,7 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
  *     of src[i]. Full pages are shared (refs + 1); a last partial page is copied
  *     into the next free page, which copy_src[i] -> copy_dst[i] says (-1, -1
  *     where there is none): run w4_kv8_copy_pages on every layer with them.
+ *     After an error all entries are -1, so that copying by them does nothing.
  * w4_kv8_free     the sequences seqs[0..n) end: their pages' refs drop by one,
  *     their table rows become -1 and their lengths 0. A sequence listed twice
  *     ends once; an empty one stays empty. (Not all or nothing: bad sequence or

@@ -252,7 +252,10 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(con
       if (offs[i] >= 0) offs[i] += c.before[1][warp_id()];
   }
   cl.sync();
-  if (err) return;
+  if (err) {  // nothing is to be copied, whatever the lists held
+    for (int i = lo + lane; i < hi; i += 32) b.copy_src[i] = b.copy_dst[i] = -1;
+    return;
+  }
   for (int i = w; i < b.n; i += NW) {  // one warp a pair
     const int s = b.list[i], d = b.list2[i], toks = held[i], off = offs[i];
     const int full = toks >> b.shift;

@@ -1,0 +1,45 @@
+"""The 8-bit key-value cache's operators where they can go wrong: calls that fail
+half-way, sequences past a bound, chained forks, one token with nearly all of the
+weight, loud pages beside quiet ones."""
+import pytest
+import torch
+
+import kv8util as ref
+from test_gpu_kv8 import agrees, book_of, cache_state, same, w4  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------- #
+# pages                                                                         #
+# --------------------------------------------------------------------------- #
+def raw_fork(w4, pool, src, dst, copy_src, copy_dst):
+    """The C call, with lists of the caller's."""
+    ws = torch.empty(w4.w4_kv8_pages_workspace_size(pool.refs.shape[0], len(src)), dtype=torch.uint8,
+                     device="cuda")
+    a, b = ref.ints(src), ref.ints(dst)
+    status = w4.lib().w4_kv8_fork(
+        pool.refs.data_ptr(), pool.refs.shape[0], pool.table.data_ptr(), pool.table.shape[1],
+        pool.lens.data_ptr(), pool.lens.shape[0], a.data_ptr(), b.data_ptr(), len(src),
+        pool.page_size, copy_src.data_ptr(), copy_dst.data_ptr(), pool.status.data_ptr(),
+        ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("src,dst,status", [
+    ([0, 1, 0], [3, 4, 5], 15),          # three partial pages, two free ones
+    ([0, 1], [3, 3], 16), ([0, 1], [3, 1], 16), ([0, 9], [3, 4], 16)])
+def test_a_failed_fork_copies_nothing(w4, src, dst, status):
+    """Its lists name no page, whatever they held: copying by them is a no-op."""
+    pool = w4.kv8_pool(7, 6, 64, 16)
+    cache = ref.random_cache(w4, 7, 2, 16, 64, seed=1)
+    w4.kv8_reserve(pool, ref.ints([40, 20, 0, 0, 0, 0]))
+    book, before = book_of(pool), cache_state(cache)
+    stale = [ref.ints([0, 1, 2][:len(src)]), ref.ints([4, 3, 5][:len(src)])]
+    raw_fork(w4, pool, src, dst, *stale)
+    assert int(pool.status) == status and agrees(pool, book)
+    w4.kv8_copy_pages(cache, *stale)
+    assert same(cache_state(cache), before)
+    assert all((x == -1).all() for x in stale)
+    assert w4.w4_device_status() == 0
