@@ -368,6 +368,16 @@ def repack_gptq(qweight, qzeros, scales, g_idx, K, N, group, dtype, layout=W4_LA
 _WORKSPACES: dict = {}
 
 
+def _on_stream(stream, idx):
+    """A context in which torch works on `stream` of device idx (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=torch.device("cuda", idx)) if stream
+                  else torch.cuda.default_stream(idx))
+    return torch.cuda.stream(stream)
+
+
 def gemm_workspace(nbytes: int, device, stream=None):
     """A workspace of at least nbytes on `device` for calls on `stream`, kept
     and reused across calls (calls on one stream run in order, so they can
@@ -381,15 +391,7 @@ def gemm_workspace(nbytes: int, device, stream=None):
     key = (idx, handle)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
-        if stream is None:
-            ctx = contextlib.nullcontext()      # the current stream is the one used
-        elif isinstance(stream, int):
-            ext = (torch.cuda.ExternalStream(stream, device=torch.device("cuda", idx)) if stream
-                   else torch.cuda.default_stream(idx))
-            ctx = torch.cuda.stream(ext)
-        else:
-            ctx = torch.cuda.stream(stream)
-        with ctx:
+        with _on_stream(stream, idx):
             ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         _WORKSPACES[key] = ws
     return ws
@@ -515,12 +517,16 @@ def _ints(x, name):
     return x.data_ptr()
 
 
-def _table(x):
-    """The address and row stride of a table [sequences, pages]."""
-    st = x.stride()
-    if len(st) != 2 or x.dtype is not _I32 or (st[1] != 1 and x.shape[1] > 1):
-        raise ValueError("the table must be int32 [sequences, pages] with adjacent pages")
-    return x.data_ptr(), st[0] if x.shape[0] > 1 else x.shape[1]
+def _table(x, stream, index):
+    """(address, pages of a row, tensor to hold on to) of a table [sequences, pages].
+    The kernels take a row's stride for its length, so columns of a wider table are
+    copied, on the call's stream."""
+    if x.dim() != 2 or x.dtype is not _I32:
+        raise ValueError("the table must be int32 [sequences, pages]")
+    if not x.is_contiguous():
+        with _on_stream(stream if index >= 0 else None, index):
+            x = x.contiguous()
+    return x.data_ptr(), x.shape[1], x
 
 
 def _batch(table, kv_lens, cu_q):
@@ -542,7 +548,7 @@ def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=No
     code = _HALF_CODES.get(dtype)
     if code is None:
         code = dtype_code(dtype)
-    tab, stride = _table(table)
+    tab, stride, held = _table(table, stream, cache._device)
     status = lib().w4_kv8_append(
         k.data_ptr(), v.data_ptr(), _rows(k, "k", hk, d), _rows(v, "v", hk, d), cache._ref, tab,
         stride, _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"), _batch(table, kv_lens, cu_q),
@@ -617,7 +623,7 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
         space, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif nbytes:
         space, nbytes = _space(nbytes, index, handle, stream)
-    tab, tab_stride = _table(table)
+    tab, tab_stride, held = _table(table, stream, index)
     status = L.w4_kv8_attention(
         q.data_ptr(), stride, cache._ref, tab, tab_stride, _ints(kv_lens, "kv_lens"),
         _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len, max_kv_len, how[1], code,
@@ -632,19 +638,21 @@ class KV8Pool:
     free page), table [sequences, pages of the longest] (-1 past a sequence's
     pages), lens [sequences] (tokens; 0: an empty slot), int32 on the GPU.
     status: an int32 tensor that receives each call's W4_OK or error (a call
-    that fails changes nothing); without one, errors go to w4_device_status."""
+    that fails changes nothing); without one, errors go to w4_device_status.
+    The three are changed in place, and table's row is a sequence's whole list of
+    pages: columns of a wider table are refused."""
 
     __slots__ = ("refs", "table", "lens", "page_size", "status", "_args", "_status", "_device",
                  "_bytes")
 
     def __init__(self, refs, table, lens, page_size, status=None):
         pages, seqs = refs.shape[0], lens.shape[0]
-        tab, stride = _table(table)
-        if table.shape[0] != seqs:
+        if table.dim() != 2 or table.shape[0] != seqs:
             raise ValueError("table must be [sequences, pages], lens [sequences]")
         self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
         self.status = status
-        self._args = (_ints(refs, "refs"), pages, tab, stride, _ints(lens, "lens"), seqs)
+        self._args = (_ints(refs, "refs"), pages, _ints(table, "table"), table.shape[1],
+                      _ints(lens, "lens"), seqs)
         self._status = None if status is None else _ints(status, "status")
         self._device = refs.get_device()
         # what any of the calls needs: at most a pair or a sequence for every slot

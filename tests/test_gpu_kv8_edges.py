@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kv8util as ref
-from test_gpu_kv8 import agrees, book_of, cache_state, same, w4  # noqa: F401
+from test_gpu_kv8 import agrees, book_of, cache_state, check, queries, same, w4  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,37 @@ def test_a_failed_fork_copies_nothing(w4, src, dst, status):
     assert same(cache_state(cache), before)
     assert all((x == -1).all() for x in stale)
     assert w4.w4_device_status() == 0
+
+
+# --------------------------------------------------------------------------- #
+# attention                                                                     #
+# --------------------------------------------------------------------------- #
+
+
+@pytest.mark.parametrize("m", [1, 100])
+def test_columns_of_a_wider_table(w4, m):
+    """A row ends where its columns end, whatever lies beside them."""
+    lens, page = [130, 60, 200], 16
+    cache = ref.random_cache(w4, 40, 2, page, 64, seed=14)
+    table = ref.scattered_table(lens, page, 40, seed=15)
+    wide = ref.ints([[0] * 30] * 3)
+    part = wide[:, 30 - table.shape[1]:]  # the last row's end is the buffer's
+    part.copy_(table)
+    q = queries(3 * m, 4, 64, "bf16", 16)
+    check(w4, q, cache, part, lens, [m] * 3, True, "bf16")
+    side = torch.cuda.Stream()
+    args = ref.ints([130, 60, 209]), ref.bounds([m] * 3), m, 1000
+    for stream in (None, side, side.cuda_stream):
+        out = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        w4.kv8_attention(q, cache, part, *args, out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert w4.w4_device_status(clear=True) == 14  # one token past the columns
+        assert torch.count_nonzero(out[2 * m:]) == 0 and torch.count_nonzero(out[:m]) > 0
+    if m == 1:
+        k = queries(3, 2, 64, "bf16", 17)
+        before = cache_state(cache)
+        w4.kv8_append(k, k, cache, part, ref.ints([0, 0, 209]), ref.ints([0, 0, 0, 1]), 1)
+        assert w4.w4_device_status(clear=True) == 14 and same(cache_state(cache), before)
+        w4.kv8_append(k, k, cache, part, ref.ints([0, 0, 200]), ref.ints([0, 0, 0, 1]), 1)
+        assert w4.w4_device_status() == 0 and not same(cache_state(cache), before)

@@ -1,0 +1,69 @@
+"""What the 8-bit cache's binding hands to the library, and what it refuses, with a
+stand-in for the library (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import int4_weight_only_repack_gb300 as w4
+
+F8 = torch.float8_e4m3fn
+
+
+class Calls:
+    """Takes any call, remembers the arguments by entry point, returns `status`."""
+
+    def __init__(self, status=0):
+        self.seen, self.status = {}, status
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.seen.setdefault(name, []).append(args)
+            return 512 if name.endswith("_size") else self.status
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    calls = Calls()
+    monkeypatch.setattr(w4, "_LIB", calls)
+    return calls
+
+
+def cache(pages=8, heads=2, page=16, dim=64):
+    codes = lambda: torch.zeros((pages, heads, page, dim), dtype=torch.uint8).view(F8)  # noqa: E731
+    return w4.KV8Cache(codes(), codes(), torch.ones(pages, heads), torch.ones(pages, heads))
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("table", [
+    torch.zeros((3, 9), dtype=torch.int32)[:, :4], torch.zeros((3, 9), dtype=torch.int32)[:, 5:],
+    torch.zeros((3, 9), dtype=torch.int32)[:, :1], torch.zeros((4, 3), dtype=torch.int32).t(),
+    torch.zeros((1, 4), dtype=torch.int32).expand(3, 4)])
+def test_a_pool_refuses_a_part_of_a_table(fake, table):
+    """Its kernels write whole rows: they would write past the columns given."""
+    with pytest.raises(ValueError):
+        w4.KV8Pool(torch.zeros(8, dtype=torch.int32), table, ints(0, 0, 0), 16)
+    w4.KV8Pool(torch.zeros(8, dtype=torch.int32), table.contiguous(), ints(0, 0, 0), 16)
+
+
+@pytest.mark.parametrize("cut", [slice(0, 4), slice(5, 9), slice(3, 4)])
+def test_columns_of_a_table_are_handed_over_as_rows_of_their_length(fake, monkeypatch, cut):
+    """append and attention must not look past the columns given."""
+    rows = []
+
+    def keep(table, stride, batch):
+        rows.append((list((ctypes.c_int * (batch * stride)).from_address(table)), stride))
+
+    wide = torch.arange(27, dtype=torch.int32).view(3, 9)
+    monkeypatch.setattr(fake, "w4_kv8_append", lambda *a: keep(a[5], a[6], 3) or 0, raising=False)
+    monkeypatch.setattr(fake, "w4_kv8_attention", lambda *a: keep(a[3], a[4], 3) or 0, raising=False)
+    c, x = cache(), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    args = (c, wide[:, cut], ints(1, 1, 1), ints(0, 1, 2, 3), 1)
+    w4.kv8_append(x, x, *args)
+    w4.kv8_attention(x, *args, 16, workspace=torch.zeros(512, dtype=torch.uint8))
+    want = (wide[:, cut].reshape(-1).tolist(), wide[:, cut].shape[1])
+    assert rows == [want, want]
