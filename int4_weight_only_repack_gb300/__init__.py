@@ -365,7 +365,7 @@ def repack_gptq(qweight, qzeros, scales, g_idx, K, N, group, dtype, layout=W4_LA
     return RepackedLayer(K, N, group, dtype, layout, qw, zeros, sc, perm, status)
 
 
-_WORKSPACES: dict = {}
+_WORKSPACES: dict = {}  # (device, stream) -> every block handed out, the largest last
 
 
 def _on_stream(stream, idx):
@@ -381,20 +381,20 @@ def _on_stream(stream, idx):
 def gemm_workspace(nbytes: int, device, stream=None):
     """A workspace of at least nbytes on `device` for calls on `stream`, kept
     and reused across calls (calls on one stream run in order, so they can
-    share it, and no call allocates device memory once it is big enough). It is
-    allocated on that stream, so when a larger one replaces it the caching
-    allocator hands the old block out again only in that stream's order (after
-    the calls that may still be reading it)."""
+    share it, and no call allocates device memory once it is big enough). A
+    block that a larger one replaces is kept too, for as long as the process
+    runs: a captured graph goes on using its address. Blocks grow by half at
+    least, so those kept are at most twice the last one."""
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
     handle = _stream(stream, idx)
     key = (idx, handle)
-    ws = _WORKSPACES.get(key)
-    if ws is None or ws.numel() < nbytes:
+    blocks = _WORKSPACES.setdefault(key, [])
+    if not blocks or blocks[-1].numel() < nbytes:
+        least = blocks[-1].numel() * 3 // 2 if blocks else 256
         with _on_stream(stream, idx):
-            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        _WORKSPACES[key] = ws
-    return ws
+            blocks.append(torch.empty(max(nbytes, least), dtype=torch.uint8, device=dev))
+    return blocks[-1]
 
 
 _WS_SIZES: dict = {}
@@ -565,7 +565,7 @@ def w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_hea
 
 _KV8_HEADS: dict = {}   # (q_heads, causal, scale) -> (struct, address)
 _KV8_SIZES: dict = {}   # arguments of a workspace size -> bytes
-_KV8_SPACES: dict = {}  # (device, stream) -> (tensor, address, bytes) of gemm_workspace
+_KV8_SPACES: dict = {}  # (device, stream) -> (address, bytes) of a block of gemm_workspace
 _KV8_KEPT = 4096
 
 
@@ -579,10 +579,10 @@ def _keep(kept, key, value):
 def _space(nbytes, index, handle, stream):
     """(address, bytes) of gemm_workspace's block for a device and stream."""
     got = _KV8_SPACES.get((index, handle))
-    if got is None or got[2] < nbytes:
+    if got is None or got[1] < nbytes:
         t = gemm_workspace(nbytes, torch.device("cuda", index), stream)
-        got = _keep(_KV8_SPACES, (index, handle), (t, t.data_ptr(), t.numel()))
-    return got[1], got[2]
+        got = _keep(_KV8_SPACES, (index, handle), (t.data_ptr(), t.numel()))
+    return got
 
 
 def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_len, scale=None,

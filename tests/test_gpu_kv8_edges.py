@@ -77,3 +77,34 @@ def test_columns_of_a_wider_table(w4, m):
         assert w4.w4_device_status(clear=True) == 14 and same(cache_state(cache), before)
         w4.kv8_append(k, k, cache, part, ref.ints([0, 0, 200]), ref.ints([0, 0, 0, 1]), 1)
         assert w4.w4_device_status() == 0 and not same(cache_state(cache), before)
+
+
+@pytest.mark.parametrize("m,n", [(1, 3000), (50, 2900)])
+def test_a_graph_outlives_the_growth_of_its_workspace(w4, m, n):
+    """A captured split call, then a call on the same stream that needs more: the
+    graph's workspace is not given to anyone else."""
+    page, dim = 64, 128
+    cache = ref.random_cache(w4, 600, 1, page, dim, seed=18)
+    table = ref.scattered_table([n, 20000], page, 600, seed=19)
+    q = queries(m, 8, dim, "bf16", 20)
+    small = (cache, table[:1], ref.ints([n]), ref.bounds([m]), m, n)
+    big_m = 300
+    big = (cache, table[1:], ref.ints([20000]), ref.bounds([big_m]), big_m, 20000)
+    size = w4.w4_kv8_attention_workspace_size(1, m, m, n, 8, 1, dim)
+    more = w4.w4_kv8_attention_workspace_size(1, big_m, big_m, 20000, 8, 1, dim)
+    assert 0 < size < more
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph, big_q = torch.cuda.CUDAGraph(), queries(big_m, 8, dim, "bf16", 21)
+    with torch.cuda.stream(side):
+        want = w4.kv8_attention(q, *small)
+        out = torch.empty_like(want)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            w4.kv8_attention(q, *small, out=out)
+        w4.kv8_attention(big_q, *big)
+        others = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        out.zero_()
+        graph.replay()
+    side.synchronize()
+    assert torch.equal(out, want) and all((x == 7).all() for x in others)

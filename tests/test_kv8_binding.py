@@ -1,6 +1,7 @@
 """What the 8-bit cache's binding hands to the library, and what it refuses, with a
 stand-in for the library (no GPU)."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -67,3 +68,25 @@ def test_columns_of_a_table_are_handed_over_as_rows_of_their_length(fake, monkey
     w4.kv8_attention(x, *args, 16, workspace=torch.zeros(512, dtype=torch.uint8))
     want = (wide[:, cut].reshape(-1).tolist(), wide[:, cut].shape[1])
     assert rows == [want, want]
+
+
+def test_a_replaced_workspace_stays(monkeypatch):
+    """A captured graph may hold its address. What is kept stays within a bound."""
+    made = []
+
+    def empty(n, dtype, device):
+        made.append((weakref.ref(t := torch.zeros(n, dtype=dtype)), n))
+        return t
+
+    monkeypatch.setattr(w4, "_WORKSPACES", {})
+    monkeypatch.setattr(w4, "_KV8_SPACES", {})
+    monkeypatch.setattr(torch, "empty", empty)
+    first = w4._space(1000, 0, None, None)
+    assert first[1] >= 1000 and w4._space(900, 0, None, None) == first
+    for n in range(1100, 40000, 100):
+        address, size = w4._space(n, 0, None, None)
+        assert size >= n
+        w4.gemm_workspace(n, torch.device("cuda", 0))
+    assert all(ref() is not None for ref, _ in made)
+    assert sum(n for _, n in made) <= 3 * made[-1][1]
+    assert address == made[-1][0]().data_ptr()
