@@ -64,6 +64,14 @@ w4_status from_cuda(cudaError_t e) {
 }
 
 w4_status check_arch() {
+  // A thread that has made no runtime call yet has no current context, and encoding
+  // a tensor map, a driver call, needs one: cudaSetDevice makes it current.
+  thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return W4_ERR_CUDA;
+    bound = true;
+  }
   DeviceInfo info;
   if (device_info(&info) != cudaSuccess) return W4_ERR_CUDA;
   if (info.major != 10 || info.minor != 3) return W4_ERR_ARCH;

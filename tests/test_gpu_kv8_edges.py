@@ -1,6 +1,8 @@
 """The 8-bit key-value cache's operators where they can go wrong: calls that fail
 half-way, sequences past a bound, chained forks, one token with nearly all of the
 weight, loud pages beside quiet ones."""
+import threading
+
 import pytest
 import torch
 
@@ -108,3 +110,26 @@ def test_a_graph_outlives_the_growth_of_its_workspace(w4, m, n):
         graph.replay()
     side.synchronize()
     assert torch.equal(out, want) and all((x == 7).all() for x in others)
+
+
+@pytest.mark.parametrize("what", ["rows", "tiles", "linear", "linear_fp8"])
+def test_a_thread_that_has_not_used_the_gpu(w4, what):
+    """Its first CUDA call may be this library's."""
+    cache = ref.random_cache(w4, 5, 1, 64, 128, seed=22)
+    table = ref.scattered_table([300], 64, 5, seed=23)
+    K, N = 256, 128
+    scales = torch.full((K // 128, N), 0.01, device="cuda", dtype=torch.bfloat16)
+    layer = w4.repack_awq(ref.ints([[7] * (N // 8)] * K), ref.ints([[5] * (N // 8)] * (K // 128)), scales, K, N,
+                          128, torch.bfloat16)
+    x = torch.ones((200, K), device="cuda", dtype=torch.bfloat16)
+    m = 200 if what == "tiles" else 1
+    q = queries(m, 4, 128, "bf16", 24)
+    args = (cache, table, ref.ints([300]), ref.bounds([m]), m, 300)
+    call = {"linear": lambda: w4.linear(x, layer), "linear_fp8": lambda: w4.linear_fp8(x, layer)}.get(
+        what, lambda: w4.kv8_attention(q, *args))
+    want, got = call(), []
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=lambda: got.append(call()))
+    thread.start()
+    thread.join()
+    assert len(got) == 1 and torch.equal(got[0], want)
