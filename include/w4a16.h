@@ -23,6 +23,11 @@
  *     returns.
  *   - All work is enqueued asynchronously on `stream` (a cudaStream_t; NULL =
  *     the legacy default stream). No call synchronises the host.
+ *   - Host threads may call at once. The kernels of a call that is given a
+ *     workspace are enqueued with no other such call's between them, so calls on
+ *     one stream may share a workspace whichever threads make them. Calls on
+ *     different streams need workspaces of their own, and so do graphs that may
+ *     be replayed at once.
  *   - Arguments are validated on the host before anything is launched. On any
  *     error the call returns a non-zero w4_status and launches nothing.
  *     Validation needs no GPU: bad arguments are reported even where no CUDA

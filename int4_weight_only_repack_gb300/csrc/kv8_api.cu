@@ -211,6 +211,7 @@ w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_cache* c
   a.bf16 = dtype == W4_BF16;
   a.scale = heads->scale;
   a.workspace = workspace;
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
   return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -284,6 +285,7 @@ w4_status w4_kv8_free(int32_t* refs, int num_pages, int32_t* table, int table_st
   if ((st = check_arch())) return st;
   BookArgs a{refs, table, lens, num_pages, table_stride, num_seqs, shift_of(page_size), seqs,
              nullptr, n, nullptr, nullptr, status_out, nullptr};
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
   return from_cuda(launch_free(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -303,6 +305,7 @@ w4_status w4_kv8_compact(int32_t* refs, int num_pages, int32_t* table, int table
   if ((st = check_arch())) return st;
   BookArgs a{refs, table, nullptr, num_pages, table_stride, num_seqs, 0, nullptr, nullptr, 0,
              copy_src, copy_dst, nullptr, workspace};
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
   return from_cuda(launch_compact(a, static_cast<cudaStream_t>(stream)));
 }
 

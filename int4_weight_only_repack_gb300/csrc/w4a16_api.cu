@@ -78,6 +78,12 @@ w4_status check_arch() {
   return W4_OK;
 }
 
+std::mutex& stream_mutex(const void* stream) {
+  static std::mutex locks[64];
+  const uintptr_t h = reinterpret_cast<uintptr_t>(stream);  // NULL and cudaStreamLegacy are one stream
+  return locks[h == 1 ? 0 : (h >> 4 ^ h >> 10) % 64];
+}
+
 cudaError_t device_info(DeviceInfo* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -402,6 +408,7 @@ w4_status gemm_impl(const void* x, const int32_t* qw, const void* scales, const 
   a.test_stall = test_stall;
   DeviceInfo info;
   if (device_info(&info) != cudaSuccess) return W4_ERR_CUDA;
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
   if (use_prefill(M, N, K, info.sm_count))
     return from_cuda(launch_prefill(a, static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_decode(a, static_cast<cudaStream_t>(stream)));
@@ -474,6 +481,7 @@ w4_status w4a8_gemm(const void* x, const int32_t* qw, const void* scales, const 
     if (overlaps(y, y_b, ins[j], in_b[j])) return W4_ERR_ALIAS;
   if (overlaps(workspace, workspace_bytes, x, (size_t)M * K * 2)) return W4_ERR_ALIAS;
   if ((st = check_arch())) return st;
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
   return from_cuda(launch_w4a8(x, reinterpret_cast<const uint32_t*>(qw), scales,
                                reinterpret_cast<const uint32_t*>(zeros), y, M, N, K, g,
                                dtype == W4_BF16, workspace, static_cast<cudaStream_t>(stream)));

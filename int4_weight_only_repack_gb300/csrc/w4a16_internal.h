@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/w4a16.h"
 
 namespace w4 {
@@ -138,5 +140,10 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 }
 w4_status check_arch();
 w4_status from_cuda(cudaError_t e);
+
+// Held while a call enqueues kernels that hand a workspace on to one another: host
+// threads may share a stream and its workspace, and another thread's call must not
+// come between. One of a few locks, chosen by the stream.
+std::mutex& stream_mutex(const void* stream);
 
 }  // namespace w4

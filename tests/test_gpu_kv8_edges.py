@@ -133,3 +133,41 @@ def test_a_thread_that_has_not_used_the_gpu(w4, what):
     thread.start()
     thread.join()
     assert len(got) == 1 and torch.equal(got[0], want)
+
+
+def test_threads_that_share_a_stream(w4):
+    """Calls of several host threads on one stream, all with the stream's workspace."""
+    page, dim, rounds = 64, 128, 150
+    cache = ref.random_cache(w4, 300, 1, page, dim, seed=22)
+    table = ref.scattered_table([2900, 9000], page, 300, seed=23)
+    K, N = 4096, 1024
+    g = torch.Generator(device="cuda").manual_seed(24)
+    words = lambda *shape: torch.randint(-2 ** 31, 2 ** 31 - 1, shape, device="cuda", generator=g,  # noqa: E731
+                                         dtype=torch.int32)
+    scales = torch.full((K // 128, N), 0.01, device="cuda", dtype=torch.bfloat16)
+    layer = w4.repack_awq(words(K, N // 8), words(K // 128, N // 8), scales, K, N, 128, torch.bfloat16)
+    assert w4.w4a16_gemm_workspace_size(128, N, K, 128, torch.bfloat16, False) > 0  # splits K
+
+    def attend(m, row, n, heads):
+        q = queries(m, heads, dim, "bf16", 25 + m)
+        args = (cache, table[row:row + 1], ref.ints([n]), ref.bounds([m]), m, n)
+        return lambda: w4.kv8_attention(q, *args)
+
+    x = torch.randn((128, K), device="cuda", generator=g).bfloat16()
+    work = [attend(1, 0, 2900, 4), attend(1, 1, 9000, 8), attend(50, 0, 2800, 8), attend(2, 1, 8000, 8),
+            lambda: w4.linear(x, layer), lambda: w4.linear_fp8(x, layer)]
+    want = [f() for f in work]
+    torch.cuda.synchronize()
+    start, right = threading.Barrier(len(work)), []
+
+    def run(f, expected):
+        start.wait()
+        got = [f() for _ in range(rounds)]
+        right.extend(1 for y in got if torch.equal(y, expected))
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(work, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(right) == len(work) * rounds and w4.w4_device_status() == 0
