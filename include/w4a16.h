@@ -477,7 +477,8 @@ W4_API w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_st
  *            Rows at or past cu_q[batch] are not written.
  *   table, kv_lens, cu_q, max_q_len as for w4_kv8_append; max_kv_len: at least
  *            every kv_lens[b], at most 2^30. A sequence beyond either bound or its table row
- *            gets zeros (W4_ERR_PAGE); a page number out of range counts as a
+ *            gets zeros (W4_ERR_PAGE); one whose offsets fall or leave 0..total_q
+ *            is left out (W4_ERR_PAGE); a page number out of range counts as a
  *            page without tokens (W4_ERR_PAGE).
  *   workspace: at least w4_kv8_attention_workspace_size(...) bytes (may be NULL
  *            when that is 0), no initialisation needed; else W4_ERR_WORKSPACE.

@@ -222,6 +222,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     seg.h = bh - seg.b * a.c.heads;
     load_items<ROWS>(a, seg);
     if (!seg.s.ok && threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
+    if (seg.s.n > a.max_q) {
+      zero_rows<D>(a, seg.s, seg.h, seg.tile, r.row_tiles);
+      return;
+    }
     if (seg.tile >= seg.tiles) return;
     seg.left = ITEM_COST + seg.units;
     cut(seg, 0);

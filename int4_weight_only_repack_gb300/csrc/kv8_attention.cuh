@@ -102,7 +102,9 @@ __device__ __forceinline__ bool zero_nan_codes(uint32_t& w) {
   return true;
 }
 
-// Sequence b of the batch, checked: rows of new tokens and cached tokens.
+// Sequence b of the batch, checked: rows of new tokens and cached tokens. One past a
+// bound has no cached tokens, so that its rows become zeros; one past max_q has more
+// rows than the grids are made for (zero_rows, or units dealt by the rows there are).
 struct Seq {
   int q0, n, kv;
   bool ok;
@@ -112,13 +114,26 @@ __device__ __forceinline__ Seq load_seq(const Attn& a, int b) {
   s.q0 = a.cu_q[b];
   s.n = a.cu_q[b + 1] - s.q0;
   s.kv = a.kv_lens[b];
-  s.ok = s.q0 >= 0 && s.n >= 0 && s.n <= a.max_q && s.q0 <= a.total_q - s.n;
+  s.ok = s.q0 >= 0 && s.n >= 0 && s.q0 <= a.total_q - s.n;
   if (!s.ok) s.n = 0;
-  if (s.kv < 0 || s.kv > a.max_kv || s.kv > ((long long)a.table_stride << a.c.page_shift)) {
+  if (s.n > a.max_q || s.kv < 0 || s.kv > a.max_kv ||
+      s.kv > ((long long)a.table_stride << a.c.page_shift)) {
     s.kv = 0;
     s.ok = false;
   }
   return s;
+}
+
+// Zeros to all rows of a sequence in the query heads of kv head h: a block's share.
+template <int D>
+__device__ void zero_rows(const Attn& a, const Seq& s, int h, int part, int parts) {
+  const int width = a.group * (D / 8);  // 16-byte pieces of a token
+  const long long all = (long long)s.n * width;
+  for (long long i = (long long)part * blockDim.x + threadIdx.x; i < all; i += (long long)parts * blockDim.x) {
+    const long long tok = i / width;
+    reinterpret_cast<uint4*>(a.out + ((size_t)(s.q0 + tok) * a.q_heads + (size_t)h * a.group) * D)[i - tok * width] =
+        make_uint4(0, 0, 0, 0);
+  }
 }
 
 }  // namespace kv8

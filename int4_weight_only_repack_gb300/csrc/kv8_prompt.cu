@@ -243,6 +243,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   const int b = bh / a.c.heads, h = bh - b * a.c.heads;
   const Seq s = load_seq(a, b);
   if (!s.ok && tid == 0 && tile == 0 && part == 0) record(a.status, W4_ERR_PAGE);
+  if (s.n > a.max_q) {
+    zero_rows<D>(a, s, h, tile * parts + part, p.tiles * parts);
+    return;
+  }
   const int rows = s.n * a.group, row0 = tile * CTA_ROWS;
   if (row0 >= rows) return;
 
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
   const int b = bh / a.c.heads, h = bh - b * a.c.heads;
   const Seq s = load_seq(a, b);
   const int row = tile * CTA_ROWS + lrow;
-  if (row >= s.n * a.group) return;
+  if (row >= s.n * a.group || s.n > a.max_q) return;
   const size_t pitch = (size_t)CTA_ROWS * (D + 2);
   const float* from = p.sums + (size_t)item * p.parts * pitch + lrow * (D + 2);
   float2 ml = make_float2(NEG_INF, 0.f);  // (at most 32 parts)

@@ -50,6 +50,21 @@ def test_a_failed_fork_copies_nothing(w4, src, dst, status):
 # --------------------------------------------------------------------------- #
 # attention                                                                     #
 # --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("heads,kv_heads,max_q,max_kv", [
+    (4, 2, 1, 200), (4, 2, 1, 3000), (16, 2, 3, 200), (16, 2, 3, 3000),  # few rows: items, runs
+    (4, 1, 33, 200), (4, 1, 33, 3000)])                                  # many: tiles, split tiles
+def test_more_new_tokens_than_the_bound_give_zeros(w4, heads, kv_heads, max_q, max_kv):
+    lens, counts = [100, 200, 150], [1, 300, max_q]
+    cache = ref.random_cache(w4, 20, kv_heads, 32, 64, seed=3)
+    table = ref.scattered_table(lens, 32, 20, seed=4)
+    q = queries(sum(counts), heads, 64, "bf16", 5)
+    out = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds(counts), max_q, max_kv, out=out)
+    assert w4.w4_device_status(clear=True) == 14
+    assert torch.count_nonzero(out[1:301]) == 0
+    want, tol = ref.attention(q, cache, table, [100, 0, 150], counts, 64 ** -0.5, True, "bf16")
+    keep = [0] + list(range(301, sum(counts)))
+    assert ((out.double() - want).abs()[keep] <= tol[keep]).all()
 
 
 @pytest.mark.parametrize("m", [1, 100])
