@@ -511,9 +511,11 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
  * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0) for every sequence, and
  *     gives it the pages that takes: the lowest free ones, sequence by sequence.
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
- *     of src[i]. Full pages are shared (refs + 1); a last partial page is copied
- *     into the next free page, which copy_src[i] -> copy_dst[i] says (-1, -1
- *     where there is none): run w4_kv8_copy_pages on every layer with them.
+ *     of src[i], which may be an earlier pair's target. Full pages are shared
+ *     (refs + 1); a last partial page is copied into the next free page, which
+ *     copy_src[i] -> copy_dst[i] says (-1, -1 where there is none; from the page
+ *     at the start of a chain, so that no copy reads what another writes): run
+ *     w4_kv8_copy_pages on every layer with them.
  *     After an error all entries are -1, so that copying by them does nothing.
  * w4_kv8_free     the sequences seqs[0..n) end: their pages' refs drop by one,
  *     their table rows become -1 and their lengths 0. A sequence listed twice

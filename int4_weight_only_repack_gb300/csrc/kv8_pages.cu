@@ -45,7 +45,7 @@ struct Counts {
   int own[2][BW];   // this CTA's warps
   int before[2][BW];  // what the cluster's warps before each of them counted
   int total[2];
-  int err;          // this CTA's error, then the cluster's
+  int err[2];       // this CTA's error, in each of two steps
 };
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
@@ -83,11 +83,11 @@ __device__ void exchange(cg::cluster_group& cl, Counts& c) {
   __syncthreads();
 }
 
-// Whether any CTA of the cluster has seen an error (the largest code wins).
-__device__ int cluster_error(cg::cluster_group& cl, Counts& c) {
+// Whether any CTA of the cluster has seen an error in a step (the largest code wins).
+__device__ int cluster_error(cg::cluster_group& cl, Counts& c, int step) {
   cl.sync();
   int e = 0;
-  for (int r = 0; r < CL; ++r) e = max(e, cl.map_shared_rank(&c, r)->err);
+  for (int r = 0; r < CL; ++r) e = max(e, cl.map_shared_rank(&c, r)->err[step]);
   return e;
 }
 
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   grid_wait();
   grid_launch_dependents();
   const int w = blockIdx.x * BW + warp_id(), lane = lane_id();
-  if (threadIdx.x == 0) c.err = 0;
+  if (threadIdx.x == 0) c.err[0] = c.err[1] = 0;
   __syncthreads();
   count_pages<false>(b, c);
   int lo, hi, need = 0;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
     const int held = b.lens[s], add = b.list[s];
     const long long sum = (long long)held + add;
     if (held < 0 || add < 0 || sum > ((long long)b.stride << b.shift))
-      atomicMax(&c.err, W4_ERR_PAGE);
+      atomicMax(&c.err[0], W4_ERR_PAGE);
     else
       need += pages_of(sum, b.shift) - pages_of(held, b.shift);
   }
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   for (int d = 16; d > 0; d >>= 1) need += __shfl_xor_sync(~0u, need, d);
   if (lane == 0) c.own[1][warp_id()] = need;
   __syncthreads();
-  int err = cluster_error(cl, c);
+  int err = cluster_error(cl, c, 0);
   exchange(cl, c);
   const int want = c.total[1];
   if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
@@ -185,65 +185,83 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   }
 }
 
+// The sequence whose tokens pair i's target gets, NONE or BAD. Targets are claimed: the
+// length of pair j's is -(j + 1). A source that an earlier pair makes has what that
+// pair copies; one that a later pair makes, or this one, is still empty.
+constexpr int NONE = -1, BAD = -2;
+__device__ __forceinline__ int root_of(const Book& b, int i) {
+  for (;;) {
+    const int s = b.list[i], claim = b.lens[s];
+    if (claim >= 0) return s;
+    const int j = -(claim + 1);
+    if (j >= b.n || b.list2[j] != s) return BAD;  // no claim, but a length below zero
+    if (j >= i) return NONE;
+    i = j;
+  }
+}
+
 __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(const Book b) {
   cg::cluster_group cl = cg::this_cluster();
   __shared__ Counts c;
   grid_wait();
   grid_launch_dependents();
   int32_t* fresh = b.ws;
-  int32_t* offs = b.ws + b.pages;  // per pair: rank of its fresh page, -1 for none
+  int32_t* offs = b.ws + b.pages;  // per pair: whether it has claimed its target; then the
+                                   // rank of its fresh page, -1 for none
   int32_t* held = offs + b.n;      // per pair: the source's tokens
+  int32_t* root = b.copy_src;      // per pair, until the copies are listed there
   const int w = blockIdx.x * BW + warp_id(), lane = lane_id();
-  if (threadIdx.x == 0) c.err = 0;
+  if (threadIdx.x == 0) c.err[0] = c.err[1] = 0;
   __syncthreads();
   count_pages<false>(b, c);
-  int lo, hi, need = 0;
+  int lo, hi;
   chunk(b.n, w, &lo, &hi);
-  for (int base = lo; base < hi; base += 32) {
-    const int i = base + lane;
-    int part = 0, toks = 0;
-    if (i < hi) {
-      const int s = b.list[i], d = b.list2[i];
-      if (s < 0 || s >= b.seqs || d < 0 || d >= b.seqs) {
-        atomicMax(&c.err, W4_ERR_SEQ);
-      } else {
-        toks = b.lens[s];
-        if (toks < 0 || toks > ((long long)b.stride << b.shift)) {
-          atomicMax(&c.err, W4_ERR_PAGE);
+  // claim the targets: each must be empty, and only one pair's
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int s = b.list[i], d = b.list2[i];
+    const bool ok = s >= 0 && s < b.seqs && d >= 0 && d < b.seqs && atomicCAS(&b.lens[d], 0, -(i + 1)) == 0;
+    offs[i] = ok;
+    if (!ok) atomicMax(&c.err[0], W4_ERR_SEQ);
+  }
+  __syncthreads();
+  int err = cluster_error(cl, c, 0);
+  const bool claimed = !err;  // every target
+  int want = 0;
+  if (!err) {
+    int need = 0;
+    for (int base = lo; base < hi; base += 32) {
+      const int i = base + lane;
+      int part = 0;
+      if (i < hi) {
+        root[i] = root_of(b, i);
+        int toks = root[i] < 0 ? 0 : b.lens[root[i]];
+        if (root[i] == BAD || toks > ((long long)b.stride << b.shift)) {
+          atomicMax(&c.err[1], W4_ERR_PAGE);
           toks = 0;
         }
         part = (toks & ((1 << b.shift) - 1)) != 0;
+        held[i] = toks;
       }
-      held[i] = toks;
+      const unsigned m = __ballot_sync(~0u, part != 0);
+      if (i < hi) offs[i] = part ? need + __popc(m & lanes_below()) : -1;  // + the warp's own start
+      need += __popc(m);
     }
-    const unsigned m = __ballot_sync(~0u, part != 0);
-    if (i < hi) offs[i] = part ? need + __popc(m & lanes_below()) : -1;  // + the warp's own start
-    need += __popc(m);
-  }
-  if (lane == 0) c.own[1][warp_id()] = need;
-  // the sources' page numbers, one warp a pair
-  for (int i = w; i < b.n; i += NW) {
-    const int s = b.list[i];
-    if (s < 0 || s >= b.seqs) continue;
-    const int n = min(pages_of(max(b.lens[s], 0), b.shift), b.stride);
-    for (int j = lane; j < n; j += 32) {
-      const int p = b.table[(size_t)s * b.stride + j];
-      if (p < 0 || p >= b.pages) atomicMax(&c.err, W4_ERR_PAGE);
+    if (lane == 0) c.own[1][warp_id()] = need;
+    // the sources' page numbers, one warp a pair
+    for (int i = w; i < b.n; i += NW) {
+      const int s = root_of(b, i);
+      if (s < 0) continue;
+      const int n = min(pages_of(b.lens[s], b.shift), b.stride);
+      for (int j = lane; j < n; j += 32) {
+        const int p = b.table[(size_t)s * b.stride + j];
+        if (p < 0 || p >= b.pages) atomicMax(&c.err[1], W4_ERR_PAGE);
+      }
     }
-  }
-  __syncthreads();
-  int err = cluster_error(cl, c);
-  exchange(cl, c);
-  const int want = c.total[1];
-  if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
-  // claim the targets: each must be empty, and only one pair's
-  if (!err) {
-    for (int i = lo + lane; i < hi; i += 32)
-      if (atomicCAS(&b.lens[b.list2[i]], 0, -(i + 1)) != 0) atomicMax(&c.err, W4_ERR_SEQ);
     __syncthreads();
-    err = cluster_error(cl, c);
-    if (err)
-      for (int i = lo + lane; i < hi; i += 32) atomicCAS(&b.lens[b.list2[i]], -(i + 1), 0);
+    err = cluster_error(cl, c, 1);
+    exchange(cl, c);
+    want = c.total[1];
+    if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
   }
   report(b, err);
   if (!err) {
@@ -252,14 +270,17 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(con
       if (offs[i] >= 0) offs[i] += c.before[1][warp_id()];
   }
   cl.sync();
-  if (err) {  // nothing is to be copied, whatever the lists held
-    for (int i = lo + lane; i < hi; i += 32) b.copy_src[i] = b.copy_dst[i] = -1;
+  if (err) {  // nothing is claimed or to be copied, whatever the lists held
+    for (int i = lo + lane; i < hi; i += 32) {
+      if (claimed || offs[i]) b.lens[b.list2[i]] = 0;
+      b.copy_src[i] = b.copy_dst[i] = -1;
+    }
     return;
   }
   for (int i = w; i < b.n; i += NW) {  // one warp a pair
-    const int s = b.list[i], d = b.list2[i], toks = held[i], off = offs[i];
+    const int s = root[i], d = b.list2[i], toks = held[i], off = offs[i];
     const int full = toks >> b.shift;
-    const int32_t* from = b.table + (size_t)s * b.stride;
+    const int32_t* from = b.table + (size_t)max(s, 0) * b.stride;
     int32_t* to = b.table + (size_t)d * b.stride;
     const int page = off >= 0 ? fresh[off] : -1;
     const int last = off >= 0 ? from[full] : -1;
@@ -273,6 +294,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(con
       }
       to[j] = p;
     }
+    __syncwarp();
     if (lane == 0) {
       b.lens[d] = toks;
       b.copy_src[i] = last;

@@ -3,6 +3,7 @@ half-way, sequences past a bound, chained forks, one token with nearly all of th
 weight, loud pages beside quiet ones."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
@@ -45,6 +46,82 @@ def test_a_failed_fork_copies_nothing(w4, src, dst, status):
     assert same(cache_state(cache), before)
     assert all((x == -1).all() for x in stale)
     assert w4.w4_device_status() == 0
+
+
+@pytest.mark.parametrize("tokens", [32, 37])
+def test_forks_in_a_chain(w4, tokens):
+    """Pairs take effect in order: a target may be a later pair's source."""
+    pool = w4.kv8_pool(20, 7, 64, 16)
+    cache = ref.random_cache(w4, 20, 2, 16, 64, seed=2)
+    w4.kv8_reserve(pool, ref.ints([0, tokens, 5, 0, 0, 0, 0]))
+    # 3 and 4 through 0, before 0's own pair nothing: 5 stays empty, and so does 6
+    src, dst = [3, 1, 0, 4, 6], [5, 0, 4, 3, 6]
+    moves = w4.kv8_fork(pool, ref.ints(src), ref.ints(dst))
+    assert int(pool.status) == 0
+    w4.kv8_copy_pages(cache, *moves)
+    assert pool.lens.tolist() == [tokens, tokens, 5, tokens, tokens, 0, 0]
+    full, part = divmod(tokens, 16)
+    table = pool.table.tolist()
+    want = [1] * full + [-1] * (4 - full)
+    for s in (0, 3, 4):
+        assert table[s][:full] == table[1][:full] and table[s][full + (part > 0):] == [-1] * (4 - full - (part > 0))
+    assert table[5] == table[6] == [-1] * 4
+    refs = [0] * 20
+    for row in table:
+        for p in row:
+            if p >= 0:
+                refs[p] += 1
+    assert pool.refs.tolist() == refs and [refs[p] for p in table[1][:full]] == [4] * full
+    if part:
+        last = [table[s][full] for s in (1, 2 - 2, 3, 4)]
+        assert len(set(last)) == 4 and all(refs[p] == 1 for p in last)
+        for p in last[1:]:
+            assert torch.equal(cache.k[p, :, :part].view(torch.uint8), cache.k[last[0], :, :part].view(torch.uint8))
+            assert torch.equal(cache.v_scale[p], cache.v_scale[last[0]])
+
+
+def fork_in_order(book, src, dst):
+    """Pair by pair. Returns the moves; a chain's copies all read its first page."""
+    first, moves = {}, []
+    for s, d in zip(src, dst):
+        full, part = divmod(book.lens[s], book.page)
+        row, move = book.table[s][:full], (-1, -1)
+        if part:
+            move = (first.get(s, book.table[s][full]), book.lowest(1)[0])
+            row.append(move[1])
+            first[d] = move[0]
+        for p in row:
+            book.refs[p] += 1
+        book.table[d], book.lens[d] = row + [-1] * (len(book.table[d]) - len(row)), book.lens[s]
+        moves.append(move)
+    return moves
+
+
+@pytest.mark.parametrize("seqs", [40, 700])
+def test_random_chains_of_forks(w4, seqs):
+    rng = np.random.default_rng(seqs)
+    pool = w4.kv8_pool(12 * seqs, seqs, 160, 16)
+    new = [int(rng.integers(1, 161)) if s < seqs // 5 else 0 for s in range(seqs)]
+    w4.kv8_reserve(pool, ref.ints(new))
+    book = book_of(pool)
+    dst = (rng.permutation(seqs - seqs // 5)[:seqs // 2] + seqs // 5).tolist()
+    src = [int(rng.choice(dst[:i + 1] if rng.random() < 0.8 else range(seqs))) for i in range(len(dst))]
+    a, b = w4.kv8_fork(pool, ref.ints(src), ref.ints(dst))
+    moves = fork_in_order(book, src, dst)
+    assert int(pool.status) == 0 and agrees(pool, book)
+    assert list(zip(a.tolist(), b.tolist())) == moves
+
+
+def test_a_fork_from_a_length_below_zero(w4):
+    pool = w4.kv8_pool(10, 4, 64, 16)
+    w4.kv8_reserve(pool, ref.ints([40, 0, 0, 0]))
+    for bad in (-1, -2, -3, -2 ** 31):
+        pool.lens[0] = bad
+        book = book_of(pool)
+        w4.kv8_fork(pool, ref.ints([0, 3]), ref.ints([2, 1]))
+        assert int(pool.status) == 14 and agrees(pool, book)
+        w4.kv8_fork(pool, ref.ints([3, 1]), ref.ints([0, 2]))  # nor is it an empty target
+        assert int(pool.status) == 16 and agrees(pool, book)
 
 
 # --------------------------------------------------------------------------- #
