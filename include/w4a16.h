@@ -520,7 +520,7 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
  * w4_kv8_free     the sequences seqs[0..n) end: their pages' refs drop by one,
  *     their table rows become -1 and their lengths 0. A sequence listed twice
  *     ends once; an empty one stays empty. (Not all or nothing: bad sequence or
- *     page numbers are skipped and reported.)
+ *     page numbers and lengths are skipped and reported.)
  * w4_kv8_compact  moves the pages in use to the front: with u pages in use,
  *     those numbered u and above go, in ascending order, to the free numbers
  *     below u, in ascending order. Rewrites refs and table and lists the moves

@@ -638,7 +638,8 @@ class KV8Pool:
     free page), table [sequences, pages of the longest] (-1 past a sequence's
     pages), lens [sequences] (tokens; 0: an empty slot), int32 on the GPU.
     status: an int32 tensor that receives each call's W4_OK or error (a call
-    that fails changes nothing); without one, errors go to w4_device_status.
+    that fails changes nothing, but kv8_free ends the sequences that it can);
+    without one, errors go to w4_device_status.
     The three are changed in place, and table's row is a sequence's whole list of
     pages: columns of a wider table are refused."""
 

@@ -319,8 +319,11 @@ __global__ void __launch_bounds__(128) free_kernel(const Book b) {
   __syncthreads();
   const long long toks = toks_sh;
   if (toks == 0) return;
-  if (toks < 0 || toks > ((long long)b.stride << b.shift)) {
-    if (threadIdx.x == 0) record(status, W4_ERR_PAGE);
+  if (toks < 0 || toks > ((long long)b.stride << b.shift)) {  // no length: left as it was
+    if (threadIdx.x == 0) {
+      b.lens[s] = toks_sh;
+      record(status, W4_ERR_PAGE);
+    }
     return;
   }
   const int n = pages_of(toks, b.shift);

@@ -124,6 +124,16 @@ def test_a_fork_from_a_length_below_zero(w4):
         assert int(pool.status) == 16 and agrees(pool, book)
 
 
+def test_a_sequence_of_a_bad_length_is_left_alone_by_free(w4):
+    pool = w4.kv8_pool(10, 3, 64, 16)
+    w4.kv8_reserve(pool, ref.ints([40, 20, 0]))
+    for bad in (65, -3):
+        pool.lens[0] = bad
+        book = book_of(pool)
+        w4.kv8_free(pool, ref.ints([0]))
+        assert int(pool.status) == 14 and agrees(pool, book)
+
+
 # --------------------------------------------------------------------------- #
 # attention                                                                     #
 # --------------------------------------------------------------------------- #
