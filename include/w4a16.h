@@ -452,8 +452,9 @@ typedef struct w4_kv8_heads {
  *            kv_heads * head_dim), so they may be slices of one projection.
  *   table    [batch][table_stride] int32; kv_lens [batch]; cu_q [batch + 1],
  *            non-decreasing from 0; max_q_len: at least every sequence's n.
- * A sequence whose n exceeds max_q_len or kv_lens[b], or whose length does not
- * fit the table, is left out (W4_ERR_PAGE). total_q == 0 or batch == 0: no-op.
+ * A sequence whose n exceeds max_q_len or kv_lens[b], whose offsets fall or leave
+ * 0..total_q, or whose length does not fit the table or is beyond 2^30, is left out
+ * (W4_ERR_PAGE). total_q == 0 or batch == 0: no-op.
  */
 W4_API w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_stride,
                                size_t v_stride, const w4_kv8_cache* cache,

@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(AT) append_kernel(const Append a) {
   const bool is_v = blockIdx.y & 1;
   const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0, kv = a.kv_lens[b];
   const int shift = a.c.page_shift;
-  if (n <= 0 && q0 >= 0) return;
-  if (q0 < 0 || n > a.max_q || q0 > a.total_q - n || n > kv ||
+  if (n == 0 && q0 >= 0) return;
+  if (q0 < 0 || n < 0 || n > a.max_q || q0 > a.total_q - n || n > kv || kv > MAX_KV ||
       kv > ((long long)a.table_stride << shift)) {
     if (threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
     return;

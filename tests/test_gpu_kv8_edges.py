@@ -273,3 +273,21 @@ def test_threads_that_share_a_stream(w4):
     for t in threads:
         t.join()
     assert len(right) == len(work) * rounds and w4.w4_device_status() == 0
+
+
+# --------------------------------------------------------------------------- #
+# append                                                                        #
+# --------------------------------------------------------------------------- #
+def test_append_reports_bad_offsets(w4):
+    """Offsets that fall, and lengths past what any cache may hold."""
+    cache = w4.kv8_cache(8, 1, 16, 64)
+    table = ref.ints([[0, 1], [2, 3], [4, 5]])
+    x = torch.ones((6, 1, 64), dtype=torch.bfloat16, device="cuda")
+    before = cache_state(cache)
+    w4.kv8_append(x, x, cache, table, ref.ints([0, 9, 0]), ref.ints([4, 4, 2, 2]), 4)
+    assert w4.w4_device_status(clear=True) == 14 and same(cache_state(cache), before)
+    # a row of 2^27 pages: the page that ends at token 2^31 has no 32-bit end
+    longest = torch.zeros((1, 1 << 27), dtype=torch.int32, device="cuda")
+    longest[0, -1] = 3
+    w4.kv8_append(x, x, cache, longest, ref.ints([2 ** 31 - 1]), ref.ints([0, 1]), 1)
+    assert w4.w4_device_status(clear=True) == 14 and same(cache_state(cache), before)
