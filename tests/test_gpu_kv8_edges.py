@@ -275,6 +275,22 @@ def test_threads_that_share_a_stream(w4):
     assert len(right) == len(work) * rounds and w4.w4_device_status() == 0
 
 
+@pytest.mark.parametrize("batch,max_kv", [(300, 900), (2100, 900), (2100, 100)])
+def test_many_sequences(w4, batch, max_kv):
+    """More sequences than a thread block has threads, and than a split call takes."""
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 40, batch)]
+    lens[3], lens[batch - 2] = max_kv, max_kv - 1
+    counts = [int(x) for x in rng.integers(0, 3, batch)]
+    counts[3] = 2
+    page = 32
+    pages = sum(-(-n // page) for n in lens)
+    cache = ref.random_cache(w4, pages, 2, page, 64, seed=9)
+    table = ref.scattered_table(lens, page, pages, seed=10)
+    q = queries(sum(counts), 4, 64, "bf16", 11)
+    check(w4, q, cache, table, lens, counts, True, "bf16")
+
+
 # --------------------------------------------------------------------------- #
 # append                                                                        #
 # --------------------------------------------------------------------------- #
@@ -291,3 +307,23 @@ def test_append_reports_bad_offsets(w4):
     longest[0, -1] = 3
     w4.kv8_append(x, x, cache, longest, ref.ints([2 ** 31 - 1]), ref.ints([0, 1]), 1)
     assert w4.w4_device_status(clear=True) == 14 and same(cache_state(cache), before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+def test_append_to_scales_that_are_no_powers_of_two(w4, dtype, dim, page):
+    """Pages written by another program: old scales that stay, and that grow."""
+    held, new = [3, page - 2, 1, 7], [2, 2, page - 1, 1]
+    lens = [a + b for a, b in zip(held, new)]
+    cache = ref.random_cache(w4, 4, 2, page, dim, seed=12, scales="any")
+    for sc in (cache.k_scale, cache.v_scale):
+        sc[:] = ref.ints([1, 3, 5, 7]).float()[:, None] / 3 * ref.ints([1, 2]).float() / 1024
+        sc[2] *= 1e4  # stays
+    state = cache_state(cache)
+    table = ref.ints([0, 1, 2, 3]).view(4, 1)
+    x = torch.from_numpy(np.random.default_rng(13).standard_normal((sum(new), 4, dim))).cuda().to(ref.DTYPES[dtype])
+    k, v = x[:, :2], x[:, 2:]
+    w4.kv8_append(k, v, cache, table, ref.ints(lens), ref.bounds(new), max(new))
+    ref.append(state, k.double().cpu().numpy(), v.double().cpu().numpy(), table.cpu().numpy(), lens, new, page)
+    assert same(cache_state(cache), state)
+    assert w4.w4_device_status() == 0
