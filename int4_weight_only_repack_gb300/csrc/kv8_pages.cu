@@ -60,8 +60,9 @@ __device__ __forceinline__ void chunk(int n, int w, int* lo, int* hi) {
 }
 
 // Exchange the warps' counts: every CTA reads all 256 of both kinds (warp 0:
-// pages, warp 1: needs), sums what lies before its own warps and in all.
-__device__ void exchange(cg::cluster_group& cl, Counts& c) {
+// pages, warp 1: needs), sums what lies before its own warps and in all. Sums stop at
+// `cap`, which is more pages than there are: needs may add up to more than 31 bits.
+__device__ void exchange(cg::cluster_group& cl, Counts& c, int cap) {
   cl.sync();
   const int rank = (int)cl.block_rank(), w = warp_id(), lane = lane_id();
   if (w < 2) {
@@ -73,10 +74,10 @@ __device__ void exchange(cg::cluster_group& cl, Counts& c) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int u = __shfl_up_sync(~0u, inc, d);
-        if (lane >= d) inc += u;
+        if (lane >= d) inc = min(inc + u, cap);
       }
-      if (r == rank) c.before[w][lane] = run + inc - v;
-      run += __shfl_sync(~0u, inc, 31);
+      if (r == rank) c.before[w][lane] = run + inc - v;  // (meant only where the total is below cap)
+      run = min(run + __shfl_sync(~0u, inc, 31), cap);
     }
     if (lane == 0) c.total[w] = run;
   }
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   __syncthreads();
   count_pages<false>(b, c);
   int lo, hi, need = 0;
+  const int cap = b.pages + 1;
   chunk(b.seqs, w, &lo, &hi);
   for (int s = lo + lane; s < hi; s += 32) {
     const int held = b.lens[s], add = b.list[s];
@@ -149,14 +151,14 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
     if (held < 0 || add < 0 || sum > ((long long)b.stride << b.shift))
       atomicMax(&c.err[0], W4_ERR_PAGE);
     else
-      need += pages_of(sum, b.shift) - pages_of(held, b.shift);
+      need = min(need + pages_of(sum, b.shift) - pages_of(held, b.shift), cap);
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) need += __shfl_xor_sync(~0u, need, d);
+  for (int d = 16; d > 0; d >>= 1) need = min(need + __shfl_xor_sync(~0u, need, d), cap);
   if (lane == 0) c.own[1][warp_id()] = need;
   __syncthreads();
   int err = cluster_error(cl, c, 0);
-  exchange(cl, c);
+  exchange(cl, c, cap);
   const int want = c.total[1];
   if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
   report(b, err);
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) fork_kernel(con
     }
     __syncthreads();
     err = cluster_error(cl, c, 1);
-    exchange(cl, c);
+    exchange(cl, c, b.pages + 1);
     want = c.total[1];
     if (!err && want > c.total[0]) err = W4_ERR_NO_PAGES;
   }
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) compact_kernel(
   if (threadIdx.x == 0) holes_sh = 0;
   count_pages<true>(b, c);
   __syncthreads();
-  exchange(cl, c);
+  exchange(cl, c, b.pages + 1);
   const int used = c.total[0];
   int lo, hi;
   chunk(b.pages, w, &lo, &hi);

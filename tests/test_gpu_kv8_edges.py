@@ -124,6 +124,23 @@ def test_a_fork_from_a_length_below_zero(w4):
         assert int(pool.status) == 16 and agrees(pool, book)
 
 
+@pytest.mark.parametrize("seqs,each", [(1 << 20, 2049), (1 << 20, 4097)])
+def test_needs_past_32_bits(w4, seqs, each):
+    """A million sequences that ask for 2^31 pages and more, or 2^32, are refused."""
+    table = torch.empty((seqs, each), dtype=torch.int32, device="cuda")
+    pool = w4.KV8Pool(ref.ints([0] * 1000), table, torch.zeros(seqs, dtype=torch.int32, device="cuda"), 16,
+                      ref.ints([0]))
+    table[5, :3] = 77
+    new = torch.full((seqs,), 16 * each, dtype=torch.int32, device="cuda")
+    w4.kv8_reserve(pool, new)
+    assert int(pool.status) == 15 and not pool.refs.any() and not pool.lens.any()
+    new.zero_()
+    new[5] = 40
+    w4.kv8_reserve(pool, new)
+    assert int(pool.status) == 0 and pool.refs[:4].tolist() == [1, 1, 1, 0]
+    assert table[5, :3].tolist() == [0, 1, 2] and int(pool.lens[5]) == 40
+
+
 def test_a_sequence_of_a_bad_length_is_left_alone_by_free(w4):
     pool = w4.kv8_pool(10, 3, 64, 16)
     w4.kv8_reserve(pool, ref.ints([40, 20, 0]))
