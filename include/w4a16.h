@@ -509,8 +509,9 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
  * `workspace`: w4_kv8_pages_workspace_size(num_pages, n) bytes, n the number of
  * sequences or pairs given (num_seqs for reserve and compact).
  *
- * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0) for every sequence, and
- *     gives it the pages that takes: the lowest free ones, sequence by sequence.
+ * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0; at most 2^30 tokens then)
+ *     for every sequence, and gives it the pages that takes: the lowest free ones,
+ *     sequence by sequence.
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
  *     of src[i], which may be an earlier pair's target. Full pages are shared
  *     (refs + 1); a last partial page is copied into the next free page, which

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   for (int s = lo + lane; s < hi; s += 32) {
     const int held = b.lens[s], add = b.list[s];
     const long long sum = (long long)held + add;
-    if (held < 0 || add < 0 || sum > ((long long)b.stride << b.shift))
+    if (held < 0 || add < 0 || sum > MAX_KV || sum > ((long long)b.stride << b.shift))
       atomicMax(&c.err[0], W4_ERR_PAGE);
     else
       need = min(need + pages_of(sum, b.shift) - pages_of(held, b.shift), cap);

@@ -141,6 +141,14 @@ def test_needs_past_32_bits(w4, seqs, each):
     assert table[5, :3].tolist() == [0, 1, 2] and int(pool.lens[5]) == 40
 
 
+def test_lengths_past_32_bits(w4):
+    table = torch.empty((1, 1 << 27), dtype=torch.int32, device="cuda")
+    pool = w4.KV8Pool(ref.ints([0] * 1000), table, ref.ints([2 ** 30]), 16, ref.ints([0]))
+    for new in (1, 2 ** 30, 2 ** 31 - 1):  # (the sums are 2^30 and up to 2^31 + 2^30)
+        w4.kv8_reserve(pool, ref.ints([new]))
+        assert int(pool.status) == 14 and int(pool.lens) == 2 ** 30 and not pool.refs.any()
+
+
 def test_a_sequence_of_a_bad_length_is_left_alone_by_free(w4):
     pool = w4.kv8_pool(10, 3, 64, 16)
     w4.kv8_reserve(pool, ref.ints([40, 20, 0]))
