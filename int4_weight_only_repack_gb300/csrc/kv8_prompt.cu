@@ -359,17 +359,18 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         *reinterpret_cast<uint4*>(q + (c / 8) * BLK + sw(lrow, c % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
-      warp_arrive(bars.qfull());
     }
+    // A row warp sees a step's keys announced before it hands over what the products of
+    // that step wait for (Q, then P of the step before): the barrier cannot go on to the
+    // step after next, two phases that look alike, while a warp has yet to look.
+    bool ok = true;
+    if (my_steps > 0) ok = __all_sync(~0u, wait_for(bars.kfull(0), 0, abort_flag, a.status));
+    warp_arrive(bars.qfull());
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lanes + 128 * i, ot = tmem + lanes + 256 + D * i;
     float m = 0.f, room = NEG_INF, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < my_steps; ++j) {
-      const int stage = j % KV_STAGES;
-      ok = wait_for(bars.kfull(stage), (j / KV_STAGES) & 1, abort_flag, a.status) &&
-           wait_for(bars.sfull(i), j & 1, abort_flag, a.status);
-      ok = __all_sync(~0u, ok);
+    for (int j = 0; ok && j < my_steps; ++j) {
+      ok = __all_sync(~0u, wait_for(bars.sfull(i), j & 1, abort_flag, a.status));
       if (!ok) break;
       tc_fence_after();
       uint32_t x[4][32];
@@ -455,8 +456,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         }
         tmem_st16(st + 16 * c, y);
       }
+      if (j + 1 < my_steps)
+        ok = wait_for(bars.kfull((j + 1) % KV_STAGES), ((j + 1) / KV_STAGES) & 1, abort_flag, a.status);
       tmem_st_wait();
       tc_fence_before();
+      if (!(ok = __all_sync(~0u, ok))) break;
       warp_arrive(bars.pfull(i));
     }
     if (ok && my_steps > 0)
