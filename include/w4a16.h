@@ -419,7 +419,8 @@ typedef struct w4_kv8_cache {
     void* k;        /* [num_pages][kv_heads][page_size][head_dim] e4m3 */
     void* v;        /* the same                                       */
     float* k_scale; /* [num_pages][kv_heads], finite and > 0          */
-    float* v_scale; /* the same                                       */
+    float* v_scale; /* the same, 2^-64 to 2^120 and, among the pages of
+                       one sequence and head, within 2^100            */
     int num_pages, page_size, kv_heads, head_dim;
 } w4_kv8_cache;
 
@@ -484,8 +485,12 @@ W4_API w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_st
  *   workspace: at least w4_kv8_attention_workspace_size(...) bytes (may be NULL
  *            when that is 0), no initialisation needed; else W4_ERR_WORKSPACE.
  * q is taken in fp16 after a power-of-two scaling of each row (exact but for
- * elements below 2^-28 of the row's largest), codes enter the products exactly, p is rounded to
- * fp16, and scores, maxima, sums and products accumulate in fp32. Deterministic.
+ * elements below 2^-28 of the row's largest), codes enter the products exactly, and
+ * scores, maxima, sums and products accumulate in fp32. For the product with the
+ * values p_j * v_scale_j is rounded to fp16, scaled so that it keeps 11 bits down to
+ * 2^-22 of the row's largest such product; of a smaller one at most 2^-33 of that
+ * largest is lost. Scores (scale * q . k) must stay below 2^27 in magnitude; their
+ * differences are as exact as fp32 holds them. Deterministic.
  */
 W4_API size_t w4_kv8_attention_workspace_size(int batch, int total_q, int max_q_len,
                                               int max_kv_len, int q_heads, int kv_heads,

@@ -442,9 +442,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     const int first_lim = a.causal ? min(s.kv, s.kv - s.n + row0 / a.group + 1) : s.kv;
 
     // The base m of the exponents is a row's maximum when it was last raised: it is
-    // raised only when a score passes it by more than 8 (p' <= 2^8 still fits fp16,
-    // and the sums are the same), so most units exchange no maximum and rescale
-    // nothing. A row's first score always raises it.
+    // raised only when a score passes it by more than P_ROOM, so most units exchange
+    // no maximum and rescale nothing. A row's first score always raises it.
     float room[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = fr[nb][i] * ksc[half], c = lv - m[nb][i];
+            const float f = fr[nb][i] * ksc[half], c = lv - m[nb][i] + P_UP;
             x[nb][half][i] = x[nb][half][i] * f + c;
             x[nb][half][2 + i] = x[nb][half][2 + i] * f + c;
           }
@@ -560,15 +559,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float y = top[nb][i];  // relative to m
+            float y = top[nb][i];  // relative to m - P_UP
             y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
             y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
             y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
             const bool first = room[nb][i] == NEG_INF;
-            if (y == NEG_INF || (!first && y <= 0.f)) y = 0.f;
-            else room[nb][i] = 8.f;
-            m[nb][i] += y;
-            const float f = first ? 0.f : ex2(-y);
+            float up = 0.f, to = 0.f;
+            if (y != NEG_INF && (first || y > P_UP)) {
+              up = y - P_UP;
+              to = P_UP;
+              room[nb][i] = P_UP + P_ROOM;
+            } else {
+              y = 0.f;
+            }
+            m[nb][i] += up;
+            const float f = first ? 0.f : ex2(-up);
             l[nb][i] *= f;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
@@ -577,8 +582,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              x[nb][half][i] -= y;
-              x[nb][half][2 + i] -= y;
+              x[nb][half][i] = x[nb][half][i] - y + to;  // (y - P_UP would round large scores)
+              x[nb][half][2 + i] = x[nb][half][2 + i] - y + to;
             }
           }
       }

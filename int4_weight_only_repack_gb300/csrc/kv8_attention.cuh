@@ -4,11 +4,20 @@
 //   k_j = kc_j ks, v_j = vc_j vs  (ks, vs: one scale per page and head).
 //
 // One pass over the cache with a running maximum. With x_j = log2(e) scale ks
-// (q . kc_j) + log2(vs) the running maximum is m = max x_j, p'_j = 2^(x_j - m),
-// and
+// (q . kc_j) + log2(vs) the running base is m, p'_j = 2^(x_j - m + P_UP), and
 //   O = sum_j p'_j vc_j,   l = sum_j p'_j / vs,   out = O / l:
 // the values' scale enters the exponent, so the codes themselves are the
-// operand of the second product and p' <= 1 fits fp16.
+// operand of the second product, and what p' is scaled by cancels.
+//
+// p' is rounded to fp16 for that product (l takes it as it is). The base is raised to
+// the largest x_j only when that passes it by more than P_ROOM, so the largest p' lies
+// between 2^P_UP and 2^(P_UP + P_ROOM) = 2^15: a token's p' keeps 11 bits down to
+// 2^-22 of the largest, and no more than 2^-33 of the largest is lost of a smaller one.
+// With p' from 1 to 2^8 instead it was 2^-25: 131072 tokens with 2^-26 each of one
+// token's weight were lost whole, and so were pages whose values' scale stands 2^26
+// below another's. Room costs nothing here and what it leaves below is precision, but
+// raising the base means rescaling O: a prompt of 8000 tokens took 448 us with P_ROOM
+// 4, 434 with 5, 427 with 6, 418 with 7, 414 with 8 (P_UP = 15 - P_ROOM, 10 for 4).
 //
 // The q_heads / kv_heads query heads that share a kv head, and the new tokens
 // of a sequence, are rows of one item: row r is token r / group, head r % group.
@@ -21,6 +30,7 @@ namespace w4 {
 namespace kv8 {
 
 constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float P_UP = 8.f, P_ROOM = 7.f;
 
 // dec::bounded_wait for barriers that hand over every microsecond or less: the
 // timer (a read of some hundred cycles) and the abort flag are looked at only

@@ -4,7 +4,7 @@
 // (row r: token r / group, head r % group, so grouped heads fill a tile too) as
 // two tiles of 128, and walks the keys in steps of 128 tokens:
 //   S = Q K^T   tcgen05.mma kind::f16, both operands in shared memory
-//   P = 2^(S f + log2(vs) - m) in fp16, written over S in tensor memory
+//   P = 2^(S f + log2(vs) - m + P_UP) in fp16, written over S in tensor memory
 //   O += P V    A operand from tensor memory, V as stored (MN-major)
 // with the two tiles half a step apart, so that one tile's products run under
 // the other's exponentials. TMEM: S / P of the tiles 0-255, O 256-511.
@@ -37,7 +37,7 @@
 // largest is known, and again in the rare step that raises the base, took 423 us.
 //
 // The base m of a row's exponents is raised only when a score passes it by more
-// than 8: then its warp rescales its rows of O in tensor memory, which has to
+// than P_ROOM: then its warp rescales its rows of O in tensor memory, which has to
 // wait for the tile's last product; otherwise it never touches O.
 //
 // Every mbarrier wait is bounded (one second): a timed-out wait records
@@ -197,6 +197,14 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
 
 // A score's factor, kept above zero: a masked score of -inf times it stays -inf.
 __device__ __forceinline__ float factor(float fr, float ks) { return fmaxf(fr * ks, 1.17549435e-38f); }
+
+// Two p' as fp16: a score's maximum and its exponent are rounded apart, so scores past
+// 2^22 could put the largest p' beyond fp16, and it saturates there.
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 
 // One arrival for a warp, after all its lanes' work (each lane has put its own
 // fence before it).
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         float up = 0.f;
         if (top != NEG_INF && (first || top > 0.f)) {
           up = top;
-          room = 8.f;
+          room = P_ROOM;
         }
         m += up;
         const float f = first ? 0.f : ex2(-up);
@@ -434,6 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           tmem_st_wait();
         }
       }
+      const float base = m - P_UP;
       uint64_t f2 = 0, add2 = 0, sum = 0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           const int n = 32 * c + k, g = n / GS;
           if (n % GS == 0) {
             const float4 z = sc[g];
-            const float f = factor(fr, z.x), add = z.y - m;
+            const float f = factor(fr, z.x), add = z.y - base;
             f2 = pack2(f, f);
             add2 = pack2(add, add);
             sum = pack2(0.f, 0.f);
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           const uint64_t e = fma2(pack2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), f2, add2);
           const float p0 = ex2(lo2(e)), p1 = ex2(hi2(e));
           sum = add2f(sum, pack2(p0, p1));
-          y[k / 2] = pack_f16(p0, p1);
+          y[k / 2] = pack_p(p0, p1);
           if (n % GS == GS - 2) l += (lo2(sum) + hi2(sum)) * sc[g].z;
         }
         tmem_st16(st + 16 * c, y);

@@ -1,6 +1,7 @@
 """The 8-bit key-value cache's operators where they can go wrong: calls that fail
 half-way, sequences past a bound, chained forks, one token with nearly all of the
 weight, loud pages beside quiet ones."""
+import math
 import threading
 
 import numpy as np
@@ -298,6 +299,93 @@ def test_threads_that_share_a_stream(w4):
     for t in threads:
         t.join()
     assert len(right) == len(work) * rounds and w4.w4_device_status() == 0
+
+
+LOW = 2.0 ** -33  # of a row's largest p_j times its value scale: what the kernels may lose of one
+
+
+def exact_row(cache, table, q, n, scale):
+    """One query head over n tokens of kv head 0, in float64: (out, tolerance).
+
+    Of a token's p, times its value scale, the kernels keep fp16's eleven bits, and
+    of what is small at least LOW of the row's largest. Scores here are small, so
+    their own rounding is below 2^-16 of p; sums take n / 16 fp32 additions."""
+    ids = table[0].long()
+    k = ref.values(cache.k, cache.k_scale, ids, 0, n)
+    code = cache.v[ids, 0].double().reshape(-1, cache.head_dim)[:n]
+    vs = cache.v_scale[ids, 0].double().repeat_interleave(cache.page_size)[:n, None]
+    s = (k @ q.double())[:, None] * scale
+    p = torch.exp(s - s.max())
+    out = (p * vs * code).sum(0) / p.sum()
+    tol = ((p * vs * code.abs()).sum(0) * (2.0 ** -11 + 2.0 ** -16 + n * 2.0 ** -27)
+           + LOW * (p * vs).max() * code.abs().sum(0)) / p.sum()
+    return out, tol + 2.0 ** -11 * out.abs() + 2.0 ** -25
+
+
+@pytest.mark.parametrize("m", [1, 2, 40])
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("at", [0, 70001])
+def test_one_token_with_nearly_all_of_the_weight(w4, m, dim, page, at):
+    """Every other token has 2^-26 of its weight; together they have 0.2 %, and the
+    whole output, since its own value is zero."""
+    n, heads = 131072, 4
+    cache = w4.kv8_cache(n // page, 1, page, dim)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    v = torch.randn((n, dim), device="cuda", generator=g) + 100
+    v[at] = 0
+    cache.v.view(torch.uint8).copy_(v.to(ref.F8).view(torch.uint8).view(cache.v.shape))
+    k = torch.zeros((n, dim), device="cuda")
+    k[at, 3] = 26
+    cache.k.view(torch.uint8).copy_(k.to(ref.F8).view(torch.uint8).view(cache.k.shape))
+    table = ref.ints(list(range(n // page))).view(1, -1)
+    q = torch.zeros((m, heads, dim), dtype=torch.float16, device="cuda")
+    q[:, :, 3] = 1
+    out = w4.kv8_attention(q, cache, table, ref.ints([n]), ref.bounds([m]), m, n, scale=math.log(2),
+                           causal=False)
+    want, tol = exact_row(cache, table, q[0, 0], n, math.log(2))
+    assert (tol < 0.05 * want.abs()).all()  # that the test can see what it looks for
+    assert ((out.double() - want).abs() <= tol).all(), (out[0, 0, :4], want[:4])
+
+
+@pytest.mark.parametrize("m", [1, 2, 70])
+@pytest.mark.parametrize("up", [18, 26])
+@pytest.mark.parametrize("spread", [0.0, 0.3])
+def test_a_loud_page_beside_quiet_ones(w4, m, up, spread):
+    """One page's values stand 2^up above the others', but not in the even columns:
+    there the quiet pages are the result."""
+    n, page, dim, heads = 1024, 64, 128, 4
+    cache = ref.random_cache(w4, n // page, 1, page, dim, seed=7)
+    cache.v_scale.fill_(2.0 ** -9)
+    cache.v_scale[5] = 2.0 ** (up - 9)
+    cache.v.view(torch.uint8)[5, :, :, ::2] = 0
+    cache.v.view(torch.uint8)[5, :, :, 1::2] = torch.full((), 1.0).to(ref.F8).view(torch.uint8).item()
+    raw = cache.v.view(torch.uint8)
+    raw &= 0x7F  # of one sign, so that nothing cancels
+    cache.k_scale.fill_(2.0 ** -6)
+    table = ref.ints(list(range(n // page))).view(1, -1)
+    q = queries(m, heads, dim, "fp16", 8) * spread
+    out = w4.kv8_attention(q, cache, table, ref.ints([n]), ref.bounds([m]), m, n, causal=False)
+    for i, h in ((0, 0), (m - 1, heads - 1)):
+        want, tol = exact_row(cache, table, q[i, h], n, dim ** -0.5)
+        assert (tol[::2] < 0.05 * want[::2].abs()).all()
+        bad = (out[i, h].double() - want).abs() > tol
+        assert not bad[::2].any() and not (bad & (want.abs() < 60000)).any()
+
+
+@pytest.mark.parametrize("m,mag", [(1, 2.0 ** 21), (70, 2.0 ** 21), (1, 2.0 ** 24), (70, 2.0 ** 24), (1, 2.0 ** 30)])
+def test_scores_that_round_by_more_than_they_differ(w4, m, mag):
+    """Whichever token wins, the result is an average of values. (Scores of up to 14
+    times mag, in steps of 2^-24 of them.)"""
+    n, page, dim, heads = 1000, 64, 128, 4
+    cache = ref.random_cache(w4, n // page + 1, 1, page, dim, seed=30)
+    table = ref.scattered_table([n], page, cache.num_pages, seed=31)
+    q = queries(m, heads, dim, "bf16", 32)
+    out = w4.kv8_attention(q, cache, table, ref.ints([n]), ref.bounds([m]), m, n, causal=False, scale=mag / 10)
+    v = ref.values(cache.v, cache.v_scale, table[0].long(), 0, n)
+    lo, hi = v.amin(0), v.amax(0)
+    edge = 2.0 ** -7 * torch.maximum(lo.abs(), hi.abs())
+    assert torch.isfinite(out).all()
+    assert ((out.double() >= lo - edge) & (out.double() <= hi + edge)).all()
 
 
 @pytest.mark.parametrize("batch,max_kv", [(300, 900), (2100, 900), (2100, 100)])
