@@ -474,6 +474,8 @@ class KV8Cache:
         if not (k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
                 and v_scale.is_contiguous()):
             raise ValueError("the cache's tensors must be contiguous")
+        if not k.device == v.device == k_scale.device == v_scale.device:
+            raise ValueError("the cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self._struct = _KV8CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
@@ -489,6 +491,21 @@ def kv8_cache(num_pages, kv_heads, page_size, head_dim, device="cuda") -> KV8Cac
     k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(_F8) for _ in range(2))
     ks, vs = (torch.ones(shape[:2], dtype=_F32, device=device) for _ in range(2))
     return KV8Cache(k, v, ks, vs)
+
+
+_CURRENT_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _one_gpu(index, *tensors):
+    """Refuses tensors that are not on GPU `index`, and a GPU that is not the current
+    one: the kernels would take their addresses for its own."""
+    for x in tensors:
+        if x.get_device() != index:
+            raise ValueError("all tensors of a call must be on the same GPU")
+    if index < 0:
+        raise ValueError("the tensors must be on a GPU")
+    if _CURRENT_DEVICE() != index:
+        raise ValueError(f"the tensors are on GPU {index}, which is not the current one")
 
 
 def _on(stream, index):
@@ -548,6 +565,7 @@ def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=No
     code = _HALF_CODES.get(dtype)
     if code is None:
         code = dtype_code(dtype)
+    _one_gpu(cache._device, k, v, table, kv_lens, cu_q)
     tab, stride, held = _table(table, stream, cache._device)
     status = lib().w4_kv8_append(
         k.data_ptr(), v.data_ptr(), _rows(k, "k", hk, d), _rows(v, "v", hk, d), cache._ref, tab,
@@ -605,6 +623,8 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with q's shape and type")
+    index = cache._device
+    _one_gpu(index, q, out, table, kv_lens, cu_q)
     how = _KV8_HEADS.get((heads, causal, scale))
     if how is None:
         struct = _KV8HeadsStruct(heads, causal, dim ** -0.5 if scale is None else scale)
@@ -616,10 +636,10 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     nbytes = _KV8_SIZES.get(key)
     if nbytes is None:
         nbytes = _keep(_KV8_SIZES, key, L.w4_kv8_attention_workspace_size(*key))
-    index = cache._device
     handle = _on(stream, index)
     space = None
     if workspace is not None:
+        _one_gpu(index, workspace)
         space, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif nbytes:
         space, nbytes = _space(nbytes, index, handle, stream)
@@ -650,6 +670,9 @@ class KV8Pool:
         pages, seqs = refs.shape[0], lens.shape[0]
         if table.dim() != 2 or table.shape[0] != seqs:
             raise ValueError("table must be [sequences, pages], lens [sequences]")
+        if not refs.device == table.device == lens.device or \
+                (status is not None and status.device != refs.device):
+            raise ValueError("the pool's tensors must be on one device")
         self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
         self.status = status
         self._args = (_ints(refs, "refs"), pages, _ints(table, "table"), table.shape[1],
@@ -679,6 +702,7 @@ def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
     takes, the lowest free ones in order."""
     if new_tokens.shape[0] != pool._args[5]:
         raise ValueError("new_tokens must have an entry for every sequence")
+    _one_gpu(pool._device, new_tokens)
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_reserve(*pool._args, _ints(new_tokens, "new_tokens"), pool.page_size,
                                   pool._status,
@@ -694,6 +718,7 @@ def kv8_fork(pool: KV8Pool, src, dst, stream=None):
     n = src.shape[0]
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
+    _one_gpu(pool._device, src, dst)
     copy_src, copy_dst = torch.empty((2, n), dtype=_I32, device=src.device).unbind()
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n,
@@ -707,6 +732,7 @@ def kv8_fork(pool: KV8Pool, src, dst, stream=None):
 
 def kv8_free(pool: KV8Pool, seqs, stream=None):
     """Ends the sequences: their pages lose a reference, their slots become empty."""
+    _one_gpu(pool._device, seqs)
     status = lib().w4_kv8_free(*pool._args, _ints(seqs, "seqs"), seqs.shape[0], pool.page_size,
                                pool._status, _on(stream, pool._device))
     if status:
@@ -716,6 +742,7 @@ def kv8_free(pool: KV8Pool, seqs, stream=None):
 def kv8_compact(pool: KV8Pool, stream=None):
     """Renumbers the pages in use to the front of the pool. Returns (copy_src,
     copy_dst) for kv8_copy_pages in every layer's cache (-1 after the last)."""
+    _one_gpu(pool._device)
     refs, pages, tab, stride, _, seqs = pool._args
     copy_src, copy_dst = torch.empty((2, pages), dtype=_I32, device=pool.refs.device).unbind()
     handle = _on(stream, pool._device)
@@ -732,6 +759,7 @@ def kv8_copy_pages(cache: KV8Cache, src, dst, stream=None):
     n = src.shape[0]
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
+    _one_gpu(cache._device, src, dst)
     status = lib().w4_kv8_copy_pages(cache._ref, _ints(src, "src"), _ints(dst, "dst"), n,
                                      _on(stream, cache._device))
     if status:

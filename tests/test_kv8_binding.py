@@ -62,6 +62,7 @@ def test_columns_of_a_table_are_handed_over_as_rows_of_their_length(fake, monkey
     wide = torch.arange(27, dtype=torch.int32).view(3, 9)
     monkeypatch.setattr(fake, "w4_kv8_append", lambda *a: keep(a[5], a[6], 3) or 0, raising=False)
     monkeypatch.setattr(fake, "w4_kv8_attention", lambda *a: keep(a[3], a[4], 3) or 0, raising=False)
+    monkeypatch.setattr(w4, "_one_gpu", lambda *_: None)  # the addresses are read here
     c, x = cache(), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
     args = (c, wide[:, cut], ints(1, 1, 1), ints(0, 1, 2, 3), 1)
     w4.kv8_append(x, x, *args)
@@ -90,3 +91,66 @@ def test_a_replaced_workspace_stays(monkeypatch):
     assert all(ref() is not None for ref, _ in made)
     assert sum(n for _, n in made) <= 3 * made[-1][1]
     assert address == made[-1][0]().data_ptr()
+
+
+class On:
+    """A tensor that says it is on GPU `index`."""
+
+    def __init__(self, x, index=0):
+        self.x, self.index = x, index
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.x, name)
+
+
+def calls(c, pool, x, table, lens, cu, more=None):
+    """Every call of the binding that hands tensors over, by its tensors' names."""
+    return [lambda: w4.kv8_append(x, x, c, table, lens, cu, 1),
+            lambda: w4.kv8_attention(x, c, table, lens, cu, 1, 16, out=x, workspace=more),
+            lambda: w4.kv8_reserve(pool, lens), lambda: w4.kv8_fork(pool, lens, lens),
+            lambda: w4.kv8_free(pool, lens), lambda: w4.kv8_copy_pages(c, lens, lens)]
+
+
+def test_tensors_that_are_not_on_the_gpu_are_refused(fake, monkeypatch):
+    """Their addresses would be followed on the GPU."""
+    monkeypatch.setattr(w4, "_CURRENT_DEVICE", lambda: 0)
+    monkeypatch.setattr(w4, "_on", lambda *_: None)
+    monkeypatch.setattr(w4, "_space", lambda *_: (0, 1 << 30))
+    c, pool = cache(), w4.KV8Pool(ints(0, 0), torch.zeros((3, 4), dtype=torch.int32), ints(0, 0, 0), 16)
+    x, table = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros((3, 4), dtype=torch.int32)
+    lens, cu, ws = ints(1, 1, 1), ints(0, 1, 2, 3), torch.zeros(512, dtype=torch.uint8)
+    for call in calls(c, pool, x, table, lens, cu, ws) + [lambda: w4.kv8_compact(pool)]:  # all on the CPU
+        with pytest.raises(ValueError):
+            call()
+    c._device = pool._device = 0
+    gpu = [On(t) for t in (x, table, lens, cu, ws)]
+    for call in calls(c, pool, *gpu):
+        call()
+    assert len(fake.seen) == 6 + 1  # and the size of attention's workspace
+    for wrong in (-1, 1):
+        for i in range(5):
+            args = [On(t.x, wrong if i == j else 0) for j, t in enumerate(gpu)]
+            uses = {0: (0, 1), 1: (0, 1), 2: range(6), 3: (0, 1), 4: (1,)}[i]
+            for j, call in enumerate(calls(c, pool, *args)):
+                if j in uses:
+                    with pytest.raises(ValueError):
+                        call()
+    monkeypatch.setattr(w4, "_CURRENT_DEVICE", lambda: 1)  # the launch would go to GPU 1
+    for call in calls(c, pool, *gpu):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_a_handle_s_tensors_are_on_one_device():
+    c = cache()
+    meta = torch.empty(c.k_scale.shape, device="meta")
+    with pytest.raises(ValueError):
+        w4.KV8Cache(c.k, c.v, c.k_scale, meta)
+    table = torch.zeros((3, 4), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        w4.KV8Pool(ints(0), table, ints(0, 0, 0), 16, torch.empty(1, dtype=torch.int32, device="meta"))
+    with pytest.raises(ValueError):
+        w4.KV8Pool(ints(0), table, torch.empty(3, dtype=torch.int32, device="meta"), 16)
