@@ -461,7 +461,16 @@ _F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 _HALF_CODES = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
 
 
-class KV8Cache:
+class _Handle:
+    """Keeps the addresses of its tensors, so its attributes cannot be set anew."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__ and not name.startswith("_"):
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be set: make a new {type(self).__name__}")
+        self.__dict__[name] = value
+
+
+class KV8Cache(_Handle):
     """One layer's cache: k and v float8_e4m3fn [pages, kv_heads, page, head_dim],
     k_scale and v_scale float32 [pages, kv_heads], all contiguous on the GPU."""
 
@@ -653,7 +662,7 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     return out
 
 
-class KV8Pool:
+class KV8Pool(_Handle):
     """The pages of a pool and the sequences that hold them: refs [pages] (0: a
     free page), table [sequences, pages of the longest] (-1 past a sequence's
     pages), lens [sequences] (tokens; 0: an empty slot), int32 on the GPU.
@@ -663,9 +672,6 @@ class KV8Pool:
     The three are changed in place, and table's row is a sequence's whole list of
     pages: columns of a wider table are refused."""
 
-    __slots__ = ("refs", "table", "lens", "page_size", "status", "_args", "_status", "_device",
-                 "_bytes")
-
     def __init__(self, refs, table, lens, page_size, status=None):
         pages, seqs = refs.shape[0], lens.shape[0]
         if table.dim() != 2 or table.shape[0] != seqs:
@@ -673,16 +679,16 @@ class KV8Pool:
         if not refs.device == table.device == lens.device or \
                 (status is not None and status.device != refs.device):
             raise ValueError("the pool's tensors must be on one device")
-        self.refs, self.table, self.lens, self.page_size = refs, table, lens, page_size
-        self.status = status
-        self._args = (_ints(refs, "refs"), pages, _ints(table, "table"), table.shape[1],
-                      _ints(lens, "lens"), seqs)
-        self._status = None if status is None else _ints(status, "status")
-        self._device = refs.get_device()
         # what any of the calls needs: at most a pair or a sequence for every slot
-        self._bytes = _KV8_SIZES.get((pages, seqs))
-        if self._bytes is None:
-            self._bytes = _keep(_KV8_SIZES, (pages, seqs), w4_kv8_pages_workspace_size(pages, seqs))
+        nbytes = _KV8_SIZES.get((pages, seqs))
+        if nbytes is None:
+            nbytes = _keep(_KV8_SIZES, (pages, seqs), w4_kv8_pages_workspace_size(pages, seqs))
+        self.__dict__.update(  # (a program may make one for every step)
+            refs=refs, table=table, lens=lens, page_size=page_size, status=status,
+            _args=(_ints(refs, "refs"), pages, _ints(table, "table"), table.shape[1],
+                   _ints(lens, "lens"), seqs),
+            _status=None if status is None else _ints(status, "status"),
+            _device=refs.get_device(), _bytes=nbytes)
 
 
 def kv8_pool(num_pages, num_seqs, max_len, page_size, device="cuda") -> KV8Pool:

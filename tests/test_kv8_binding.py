@@ -154,3 +154,19 @@ def test_a_handle_s_tensors_are_on_one_device():
         w4.KV8Pool(ints(0), table, ints(0, 0, 0), 16, torch.empty(1, dtype=torch.int32, device="meta"))
     with pytest.raises(ValueError):
         w4.KV8Pool(ints(0), table, torch.empty(3, dtype=torch.int32, device="meta"), 16)
+
+
+def test_a_handle_s_attributes_cannot_be_set():
+    """Its addresses stay those of the tensors it was made of."""
+    c = cache()
+    pool = w4.KV8Pool(ints(0, 0), torch.zeros((3, 4), dtype=torch.int32), ints(0, 0, 0), 16)
+    for handle, names in ((c, "k v k_scale v_scale num_pages page_size kv_heads head_dim"),
+                          (pool, "refs table lens status page_size")):
+        for name in names.split():
+            was = getattr(handle, name)
+            with pytest.raises(AttributeError):
+                setattr(handle, name, was)
+            assert getattr(handle, name) is was
+    pool.lens[0], c.k_scale[1] = 5, 2.0  # their contents can
+    c.layer = 7
+    assert c.layer == 7
