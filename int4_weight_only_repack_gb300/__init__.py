@@ -649,6 +649,8 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     space = None
     if workspace is not None:
         _one_gpu(index, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
         space, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif nbytes:
         space, nbytes = _space(nbytes, index, handle, stream)

@@ -170,3 +170,12 @@ def test_a_handle_s_attributes_cannot_be_set():
     pool.lens[0], c.k_scale[1] = 5, 2.0  # their contents can
     c.layer = 7
     assert c.layer == 7
+
+
+def test_a_workspace_with_holes_is_refused(fake, monkeypatch):
+    """Its bytes are counted as if they were adjacent."""
+    monkeypatch.setattr(w4, "_one_gpu", lambda *_: None)
+    x, table = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros((3, 4), dtype=torch.int32)
+    room = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
+    with pytest.raises(ValueError):
+        w4.kv8_attention(x, cache(), table, ints(1, 1, 1), ints(0, 1, 2, 3), 1, 16, workspace=room)
