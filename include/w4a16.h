@@ -505,7 +505,8 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
 /*
  * The pages of a pool are counted by refs [num_pages] int32 (0: free), and its
  * sequences described by table [num_seqs][table_stride] and lens [num_seqs]
- * (tokens held; 0: an empty slot). Table entries past a sequence's pages are -1.
+ * (tokens held; 0: an empty slot). Table entries past a sequence's pages are -1: lens
+ * is what says how many there are, so lowering it by hand loses the pages beyond.
  * All four are device arrays that these calls change in place; every layer's
  * cache uses the same page numbers. Each call is all or nothing: on an error it
  * changes nothing. *status_out (device int32) receives W4_OK or the error, in
@@ -516,7 +517,8 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
  *
  * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0; at most 2^30 tokens then)
  *     for every sequence, and gives it the pages that takes: the lowest free ones,
- *     sequence by sequence.
+ *     sequence by sequence. (After an error lens is what it was, and an append that
+ *     still follows, in a graph say, takes the last tokens counted there for its own.)
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
  *     of src[i], which may be an earlier pair's target. Full pages are shared
  *     (refs + 1); a last partial page is copied into the next free page, which

@@ -8,9 +8,9 @@
 // only rounding is the one to e4m3; codes that were in the page before are read
 // and stored again only when the scale grows.
 //
-// Bound by latency for the decode step (a few hundred bytes a unit: 2.6 us in a
+// Bound by latency for the decode step (a few hundred bytes a unit: 3 us in a
 // graph for 64 tokens of 8 heads) and by HBM for prompts (2 bytes read, 1 written
-// an element): 191 MB in 29.9 us, 6.4 TB/s. What counts there is the instructions
+// an element): 191 MB in 30.3 us, 6.3 TB/s. What counts there is the instructions
 // an element. Magnitudes are compared as packed 16-bit integers and the product
 // with the power of two is taken in packed bf16; what is rare (infinities and NaN
 // that must not set the scale, an old scale that is no power of two) reads its

@@ -40,7 +40,13 @@ using dec::drain_wait;
 constexpr int WARPS = 4, THREADS = WARPS * 32, STEP = 32, STAGES = 2;
 constexpr int MAX_SMS = 160;       // that a split call uses
 constexpr int MAX_SCAN = 2048;     // sequences of a split call: every CTA scans their lengths
-constexpr int ITEM_TOKENS = 512;   // sequences up to this long are not split
+// Sequences up to this long are not split. Not split against split, in us: 1 sequence
+// of 32 heads on 32, 3.8 / 10.3 at 128 tokens, 6.6 / 11.2 at 512, 10.1 / 11.5 at 1024,
+// 17.1 / 12.5 at 2048; 64 of 64 on 8, 8.1 / 13.7, 14.7 / 19.1, 28.0 / 33.6 and 47.5 /
+// 54.2; 256 of 32 on 8, 26 / 19, 57 / 53, 92 / 95 and 165 / 179. Those are batches of
+// one length, the best that can happen to a call that is not split: where lengths
+// differ, its longest item is its time.
+constexpr int ITEM_TOKENS = 512;
 // Of a warp's run in a split call. 24 sequences of 35 to 3001 tokens, 1 to 6 new,
 // groups of 7: 17.1 us with 3 and 4, 18.2 with 6, 21.6 with 10, 26.2 with 16.
 constexpr int MIN_COST = 4;
@@ -847,7 +853,16 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const __grid_constant__ R
   }
 }
 
-// Which kernel a call runs.
+// Which kernel a call runs: this one, whose 16-row tiles each read and widen the cache
+// again, or that of kv8_prompt.cu. Here against there, in us, 32 heads on 8 of 128:
+//   rows            16            32            48            64            80           128
+//   1 x  1000  17.3 / 18.3   17.5 / 18.5   18.0 / 18.9   18.1 / 19.6   18.7 / 19.7   20.2 / 20.7
+//   1 x  8000  18.4 / 19.4   19.8 / 21.6   21.2 / 25.7   23.3 / 26.6   26.2 / 27.5   34.2 / 29.6
+//   1 x 64000  37.9 / 55.9   54.3 / 58.3   73.0 / 62.3   93.3 / 63.5    111 / 64.3    169 / 66.9
+//  16 x  1000  20.6 / 20.9   27.3 / 21.0   32.7 / 21.4   38.6 / 21.6   43.4 / 21.7   60.7 / 22.4
+//  16 x  8000  57.4 /  109   98.3 /  110    137 /  111    175 /  111    214 /  110    331 /  112
+// A border of 64 suits a single sequence of some thousand tokens; batches and long
+// caches would do better with 32, and a call whose sequences differ with both kernels.
 bool many_rows(int max_q, int group) { return (long long)max_q * group > 64; }
 
 bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX_SCAN; }

@@ -25,16 +25,18 @@
 // items as SMs, an item's steps are dealt to several CTAs, whose sums a second
 // kernel joins.
 //
-// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 416 us,
-// 1260 TFLOP/s, 66 % of the cuBLAS rate. A step takes about 3250 cycles where its
+// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 417 to
+// 422 us, 1250 TFLOP/s, 65 % of the cuBLAS rate. A step takes about 3250 cycles where its
 // products alone are 2048, and a CTA about 9 us beyond its steps (its first codes
 // and queries, the first step, the output; reading its first page numbers and
 // scales before the barriers are set up is worth 2 to 6 us a call). Neither the
 // exponentials nor the widening is what a step waits for: of 419 us, a build without
 // the first took 399, one without the second 414. It is the chain of a tile: S, from
-// tensor memory to registers and back, P V, which tensor memory (full with two
-// tiles) does not let overlap itself. Taking the exponentials before the row's
-// largest is known, and again in the rare step that raises the base, took 423 us.
+// tensor memory to registers and back, P V, and only behind that the next S, which is
+// written where P lies. (P takes half of the columns of S; the other half, and 128
+// columns where D is 64, are not used meanwhile. Half of the next S would fit there.)
+// Taking the exponentials before the row's largest is known, and again in the rare
+// step that raises the base, took 423 us.
 //
 // The base m of a row's exponents is raised only when a score passes it by more
 // than P_ROOM: then its warp rescales its rows of O in tensor memory, which has to
