@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         for (int i = 0; i < 4; ++i)
           if (absent(j, slot, i)) clear(i);
       }
+      fence_proxy_async_smem();  // the reads of the codes precede the copy that replaces them
       warp_arrive(bars.rawfree(0));
       if (!wait_warp(bars.kfree(stage), ph)) break;
       widen(L::OFF_K + stage * NB * BLK);
@@ -609,6 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
           if (edge) nan_in(i);
         }
       }
+      fence_proxy_async_smem();
       warp_arrive(bars.rawfree(1));
       if (!wait_warp(bars.vfree(stage), ph)) break;
       widen(L::OFF_V + stage * NB * BLK);

@@ -301,6 +301,26 @@ def test_threads_that_share_a_stream(w4):
     assert len(right) == len(work) * rounds and w4.w4_device_status() == 0
 
 
+@pytest.mark.parametrize("kv_heads,dim,page", [(3, 64, 32), (3, 64, 16), (2, 128, 64)])
+def test_codes_are_not_replaced_before_they_are_read(w4, kv_heads, dim, page):
+    """Many ragged sequences of a few steps each, all scores equal: every call gives
+    the same, the mean of the values that a row sees."""
+    rng = np.random.default_rng(dim + page)
+    lens = [int(x) for x in rng.integers(130, 521, 70)]
+    counts = [int(x) for x in rng.integers(20, 59, 70)]
+    pages = sum(-(-n // page) for n in lens)
+    cache = ref.random_cache(w4, pages, kv_heads, page, dim, seed=33, scales="any")
+    table = ref.scattered_table(lens, page, pages, seed=34)
+    q = queries(sum(counts), 16 * kv_heads, dim, "fp16", 35)
+    want = check(w4, q, cache, table, lens, counts, True, "fp16", scale=0.0)
+    args = (cache, table, ref.ints(lens), ref.bounds(counts), max(counts), max(lens))
+    outs = [torch.empty_like(want) for _ in range(20)]
+    for _ in range(20):
+        for out in outs:
+            w4.kv8_attention(q, *args, scale=0.0, out=out)
+        assert all(torch.equal(out, want) for out in outs)
+
+
 LOW = 2.0 ** -33  # of a row's largest p_j times its value scale: what the kernels may lose of one
 
 
