@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
           }
         }
       __syncwarp();
+      if (lane == 0) fence_proxy_async_smem();  // the reads of the stage precede its refill
       issue();  // into the stage just read
 
 #pragma unroll

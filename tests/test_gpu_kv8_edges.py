@@ -321,6 +321,24 @@ def test_codes_are_not_replaced_before_they_are_read(w4, kv_heads, dim, page):
         assert all(torch.equal(out, want) for out in outs)
 
 
+@pytest.mark.parametrize("batch,heads,dim,page", [(64, 8, 128, 64), (64, 16, 64, 16), (3, 8, 128, 128)])
+def test_units_are_not_replaced_before_they_are_read(w4, batch, heads, dim, page):
+    """The same for few rows, split among warps."""
+    rng = np.random.default_rng(batch + dim)
+    lens = [int(x) for x in rng.integers(30, 120000 // batch, batch)]
+    pages = sum(-(-n // page) for n in lens)
+    cache = ref.random_cache(w4, pages, 2, page, dim, seed=36, scales="any")
+    table = ref.scattered_table(lens, page, pages, seed=37)
+    q = queries(batch, 2 * heads, dim, "bf16", 38)
+    want = check(w4, q, cache, table, lens, [1] * batch, True, "bf16", scale=0.0)
+    args = (cache, table, ref.ints(lens), ref.bounds([1] * batch), 1, max(lens))
+    outs = [torch.empty_like(want) for _ in range(20)]
+    for _ in range(20):
+        for out in outs:
+            w4.kv8_attention(q, *args, scale=0.0, out=out)
+        assert all(torch.equal(out, want) for out in outs)
+
+
 LOW = 2.0 ** -33  # of a row's largest p_j times its value scale: what the kernels may lose of one
 
 
