@@ -524,6 +524,17 @@ def _on(stream, index):
     return _stream(stream, index if index >= 0 else None)
 
 
+def _new(make, stream, index):
+    """make()'s tensor for a call on `stream`: allocated there, so that nothing that still
+    runs on the current stream uses its memory, and kept for both when it is let go."""
+    if stream is None:
+        return make()
+    with _on_stream(stream, index):
+        x = make()
+    x.record_stream(torch.cuda.current_stream(index))
+    return x
+
+
 def _rows(x, name, heads, dim):
     """The token stride of x [tokens, heads, dim], whose rows may be slices of a
     wider buffer but whose heads and elements are adjacent."""
@@ -628,12 +639,12 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     code = _HALF_CODES.get(dtype)
     if code is None:
         code = dtype_code(dtype)
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
+    if out is not None and (out.shape != shape or out.dtype is not dtype or not out.is_contiguous()):
         raise ValueError("out must be contiguous, with q's shape and type")
     index = cache._device
-    _one_gpu(index, q, out, table, kv_lens, cu_q)
+    _one_gpu(index, q, q if out is None else out, table, kv_lens, cu_q)
+    if out is None:
+        out = _new(lambda: torch.empty_like(q, memory_format=torch.contiguous_format), stream, index)
     how = _KV8_HEADS.get((heads, causal, scale))
     if how is None:
         struct = _KV8HeadsStruct(heads, causal, dim ** -0.5 if scale is None else scale)
@@ -727,7 +738,8 @@ def kv8_fork(pool: KV8Pool, src, dst, stream=None):
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
     _one_gpu(pool._device, src, dst)
-    copy_src, copy_dst = torch.empty((2, n), dtype=_I32, device=src.device).unbind()
+    copy_src, copy_dst = _new(lambda: torch.empty((2, n), dtype=_I32, device=src.device), stream,
+                              pool._device).unbind()
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_fork(*pool._args, _ints(src, "src"), _ints(dst, "dst"), n,
                                pool.page_size, copy_src.data_ptr(), copy_dst.data_ptr(),
@@ -752,7 +764,8 @@ def kv8_compact(pool: KV8Pool, stream=None):
     copy_dst) for kv8_copy_pages in every layer's cache (-1 after the last)."""
     _one_gpu(pool._device)
     refs, pages, tab, stride, _, seqs = pool._args
-    copy_src, copy_dst = torch.empty((2, pages), dtype=_I32, device=pool.refs.device).unbind()
+    copy_src, copy_dst = _new(lambda: torch.empty((2, pages), dtype=_I32, device=pool.refs.device),
+                              stream, pool._device).unbind()
     handle = _on(stream, pool._device)
     status = lib().w4_kv8_compact(refs, pages, tab, stride, seqs, copy_src.data_ptr(),
                                   copy_dst.data_ptr(),

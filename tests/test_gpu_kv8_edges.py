@@ -339,6 +339,34 @@ def test_units_are_not_replaced_before_they_are_read(w4, batch, heads, dim, page
         assert all(torch.equal(out, want) for out in outs)
 
 
+def test_outputs_of_a_call_on_another_stream(w4):
+    """The current stream still works on a block of the output's size that it let go
+    of, and the output is used on both streams and let go of in turn."""
+    n, m = 500, 64
+    cache = ref.random_cache(w4, 10, 2, 64, 128, seed=39)
+    table = ref.scattered_table([n], 64, 10, seed=40)
+    q = queries(m, 8, 128, "bf16", 41)
+    args = (cache, table, ref.ints([n]), ref.bounds([m]), m, n)
+    want = w4.kv8_attention(q, *args)
+    side, a = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(20):
+            a @ a
+        block = torch.empty_like(want)
+        block.fill_(7)
+        del block
+        out = w4.kv8_attention(q, *args, stream=side)
+        with torch.cuda.stream(side):
+            mine = out.clone()
+        torch.cuda.current_stream().wait_stream(side)
+        yours = out.clone()
+        del out
+        other = w4.kv8_attention(q, *args, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(mine, want) and torch.equal(yours, want) and torch.equal(other, want)
+
+
 LOW = 2.0 ** -33  # of a row's largest p_j times its value scale: what the kernels may lose of one
 
 

@@ -1,5 +1,6 @@
 """What the 8-bit cache's binding hands to the library, and what it refuses, with a
 stand-in for the library (no GPU)."""
+import contextlib
 import ctypes
 import weakref
 
@@ -179,3 +180,36 @@ def test_a_workspace_with_holes_is_refused(fake, monkeypatch):
     room = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
     with pytest.raises(ValueError):
         w4.kv8_attention(x, cache(), table, ints(1, 1, 1), ints(0, 1, 2, 3), 1, 16, workspace=room)
+
+
+def test_a_call_s_outputs_are_made_on_its_stream(fake, monkeypatch):
+    """On the current stream they could be memory that work still running there uses."""
+    where, made, recorded = [None], [], []
+
+    @contextlib.contextmanager
+    def on_stream(stream, index):
+        where.append(stream)
+        yield
+        where.pop()
+
+    def make(real):
+        def call(*args, **kw):
+            made.append(where[-1])
+            return real(*args, **kw)
+        return call
+
+    monkeypatch.setattr(w4, "_on_stream", on_stream)
+    monkeypatch.setattr(w4, "_one_gpu", lambda *_: None)
+    monkeypatch.setattr(w4, "_on", lambda *_: None)
+    monkeypatch.setattr(w4, "_space", lambda *_: (0, 1 << 30))
+    monkeypatch.setattr(torch, "empty", make(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", make(torch.empty_like))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: recorded.append(s))
+    c, pool = cache(), w4.KV8Pool(ints(0, 0), torch.zeros((3, 4), dtype=torch.int32), ints(0, 0, 0), 16)
+    x, table = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros((3, 4), dtype=torch.int32)
+    for stream in (None, "side"):
+        w4.kv8_attention(x, c, table, ints(1, 1, 1), ints(0, 1, 2, 3), 1, 16, stream=stream)
+        w4.kv8_fork(pool, ints(0), ints(1), stream=stream)
+        w4.kv8_compact(pool, stream=stream)
+    assert made == [None] * 3 + ["side"] * 3 and recorded == ["current"] * 3
