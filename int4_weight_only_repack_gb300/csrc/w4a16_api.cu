@@ -78,10 +78,11 @@ w4_status check_arch() {
   return W4_OK;
 }
 
+static std::mutex g_stream_locks[64];
+
 std::mutex& stream_mutex(const void* stream) {
-  static std::mutex locks[64];
   const uintptr_t h = reinterpret_cast<uintptr_t>(stream);  // NULL and cudaStreamLegacy are one stream
-  return locks[h == 1 ? 0 : (h >> 4 ^ h >> 10) % 64];
+  return g_stream_locks[h == 1 ? 0 : (h >> 4 ^ h >> 10) % 64];
 }
 
 cudaError_t device_info(DeviceInfo* out) {
@@ -408,7 +409,8 @@ w4_status gemm_impl(const void* x, const int32_t* qw, const void* scales, const 
   a.test_stall = test_stall;
   DeviceInfo info;
   if (device_info(&info) != cudaSuccess) return W4_ERR_CUDA;
-  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
+  std::unique_lock<std::mutex> lock;
+  if (workspace) lock = std::unique_lock<std::mutex>(stream_mutex(stream));
   if (use_prefill(M, N, K, info.sm_count))
     return from_cuda(launch_prefill(a, static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_decode(a, static_cast<cudaStream_t>(stream)));
