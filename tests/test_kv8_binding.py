@@ -29,6 +29,8 @@ class Calls:
 def fake(monkeypatch):
     calls = Calls()
     monkeypatch.setattr(w4, "_LIB", calls)
+    monkeypatch.setattr(w4, "_KV8_SIZES", {})  # (its sizes are not the library's)
+    monkeypatch.setattr(w4, "_KV8_SPACES", {})
     return calls
 
 
@@ -145,7 +147,7 @@ def test_tensors_that_are_not_on_the_gpu_are_refused(fake, monkeypatch):
             call()
 
 
-def test_a_handle_s_tensors_are_on_one_device():
+def test_a_handle_s_tensors_are_on_one_device(fake):
     c = cache()
     meta = torch.empty(c.k_scale.shape, device="meta")
     with pytest.raises(ValueError):
@@ -157,7 +159,7 @@ def test_a_handle_s_tensors_are_on_one_device():
         w4.KV8Pool(ints(0), table, torch.empty(3, dtype=torch.int32, device="meta"), 16)
 
 
-def test_a_handle_s_attributes_cannot_be_set():
+def test_a_handle_s_attributes_cannot_be_set(fake):
     """Its addresses stay those of the tensors it was made of."""
     c = cache()
     pool = w4.KV8Pool(ints(0, 0), torch.zeros((3, 4), dtype=torch.int32), ints(0, 0, 0), 16)
