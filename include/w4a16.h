@@ -110,8 +110,9 @@ enum {
     W4_ERR_PAGE = 14,      /* (device) w4_kv8_*: a page number, length or offset read on
                               the device was out of range                             */
     W4_ERR_NO_PAGES = 15,  /* (device) w4_kv8_reserve / _fork: too few free pages       */
-    W4_ERR_SEQ = 16        /* (device) w4_kv8_*: a sequence number was out of range, or a
+    W4_ERR_SEQ = 16,       /* (device) w4_kv8_*: a sequence number was out of range, or a
                               fork's target was not empty or listed twice             */
+    W4_ERR_POSITION = 17   /* (device) w4_qk_norm_rope: a position past the table     */
 };
 
 enum { W4_F16 = 0, W4_BF16 = 1 };
@@ -430,6 +431,48 @@ typedef struct w4_kv8_heads {
     int causal;  /* 0 or 1                               */
     float scale; /* applied to q . k; finite             */
 } w4_kv8_heads;
+
+/* One side (queries or keys) of w4_qk_norm_rope: a HOST struct, read during the call. */
+typedef struct w4_head_rows {
+    const void* in;        /* [tokens][heads][head_dim] in dtype                     */
+    void* out;             /* the same shape                                         */
+    size_t in_stride;      /* elements from token to token: a multiple of 8, at least
+                              heads * head_dim                                       */
+    size_t out_stride;     /* the same                                               */
+    const float* weight;   /* [head_dim], of the norm; NULL: no norm on this side    */
+    int heads;             /* 1..1024                                                */
+} w4_head_rows;
+
+/* What it does to them (a HOST struct, read during the call). */
+typedef struct w4_norm_rope {
+    const float* table; /* [rows][rot_dim]: the cosines of a position's rot_dim / 2
+                           angles, then their sines; NULL: no rotation               */
+    int rows;
+    int rot_dim;        /* elements of a head that turn: a multiple of 16, 16..head_dim */
+    int interleaved;    /* 0: elements j and j + rot_dim / 2 are pair j; 1: 2 j and 2 j + 1 */
+    float eps;          /* of the norms: finite, at least 0                          */
+} w4_norm_rope;
+
+/*
+ * What stands between a layer's projection and the cache: the norm of each query and
+ * key head, and the rotation by its token's position, in one pass. For every token
+ * and head x:
+ *     y = x * (mean(x^2) + eps)^-1/2 * weight        (y = x on a side without weight)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)       for the pairs (a, b) of y
+ * in fp32 (the squares' sum too: elements up to 2^60), rounded once to dtype.
+ *   q, k       either may be NULL, for the other side alone. out may be in itself
+ *              (the same address and stride); otherwise it overlaps no input. Both
+ *              sides may be slices of one projection's rows.
+ *   how        with neither a table nor a weight on some side: W4_ERR_NULL.
+ *   positions  [tokens] int32 (4-byte alignment will do). A token whose position is below 0
+ *              is padding: its rows are not written. One at or past the table's rows
+ *              is not written either (W4_ERR_POSITION in the device status word).
+ *              May be NULL without a table: then every token's rows are written.
+ * tokens 0..2^24 (0: no-op); head_dim 64 or 128. table and weights 16-byte aligned.
+ */
+W4_API w4_status w4_qk_norm_rope(const w4_head_rows* q, const w4_head_rows* k,
+                                 const w4_norm_rope* how, const int32_t* positions, int tokens,
+                                 int head_dim, int dtype, void* stream);
 
 /*
  * Quantise new keys and values into the cache. The batch's new tokens are

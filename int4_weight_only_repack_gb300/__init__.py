@@ -26,7 +26,7 @@ __all__ = [
     "repack_awq_experts", "moe_linear",
     "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "w4_kv8_attention_workspace_size",
     "KV8Pool", "kv8_pool", "kv8_reserve", "kv8_fork", "kv8_free", "kv8_compact", "kv8_copy_pages",
-    "w4_kv8_pages_workspace_size",
+    "w4_kv8_pages_workspace_size", "qk_norm_rope", "rope_table",
 ]
 
 W4_F16, W4_BF16 = 0, 1
@@ -51,6 +51,18 @@ class _KV8CacheStruct(ctypes.Structure):
 class _KV8HeadsStruct(ctypes.Structure):
     """w4_kv8_heads."""
     _fields_ = [("q_heads", _c_int), ("causal", _c_int), ("scale", ctypes.c_float)]
+
+
+class _HeadRowsStruct(ctypes.Structure):
+    """w4_head_rows."""
+    _fields_ = [("in_", _c_void_p), ("out", _c_void_p), ("in_stride", _c_size),
+                ("out_stride", _c_size), ("weight", _c_void_p), ("heads", _c_int)]
+
+
+class _NormRopeStruct(ctypes.Structure):
+    """w4_norm_rope."""
+    _fields_ = [("table", _c_void_p), ("rows", _c_int), ("rot_dim", _c_int),
+                ("interleaved", _c_int), ("eps", ctypes.c_float)]
 
 
 _SIGNATURES = {
@@ -86,6 +98,8 @@ _SIGNATURES = {
     "w4a8_gemm_workspace_size": (_c_size, [_c_int, _c_int]),
     "w4a8_gemm": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int,
                            _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "w4_qk_norm_rope": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int,
+                                 _c_int, _c_void_p]),
     "w4_kv8_append": (_c_int, [_c_void_p, _c_void_p, _c_size, _c_size, _c_void_p, _c_void_p, _c_int,
                                _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p]),
     "w4_kv8_attention_workspace_size": (_c_size, [_c_int] * 7),
@@ -593,6 +607,76 @@ def kv8_append(k, v, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, stream=No
         k.shape[0], max_q_len, code, _on(stream, cache._device))
     if status:
         _check(status)
+
+
+def rope_table(rows, rot_dim, base=10000.0, device="cuda"):
+    """The table of qk_norm_rope: float32 [rows, rot_dim], for each position the cosines
+    of its rot_dim / 2 angles, then their sines. Pair j's angle is position *
+    base ** (-2 j / rot_dim), computed in 64 bits."""
+    rate = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * rate
+    return torch.cat((angle.cos(), angle.sin()), 1).float()
+
+
+def _side(x, name, weight, out, index, stream, held):
+    """The w4_head_rows of x [tokens, heads, dim] and its output, made if None."""
+    if out is None:
+        out = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, index)
+    elif out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError(f"{name}_out must have {name}'s shape and type")
+    _, heads, dim = x.shape
+    at = None
+    if weight is not None:
+        if weight.shape != (dim,) or weight.dtype is not _F32 or not weight.is_contiguous():
+            raise ValueError(f"{name}_weight must be contiguous float32 [{dim}]")
+        _one_gpu(index, weight)
+        at = weight.data_ptr()
+    held.append(_HeadRowsStruct(x.data_ptr(), out.data_ptr(), _rows(x, name, heads, dim),
+                                _rows(out, name + "_out", heads, dim), at, heads))
+    return out
+
+
+def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """Norms the heads of q [tokens, q_heads, dim] and k [tokens, kv_heads, dim] (fp16 or
+    bf16; either may be None) and turns them by their tokens' positions, in one pass.
+    Returns (q_out, k_out), which may be q and k themselves, or slices of one buffer.
+    positions: int32 [tokens]; below 0: padding, whose rows are not written.
+    table: float32 [rows, rot_dim], cosines and sines by position (rope_table); None: no
+    rotation, then positions may be None. q_weight, k_weight: float32 [dim] of the norms;
+    None: no norm. See w4_qk_norm_rope in include/w4a16.h."""
+    x = k if q is None else q
+    if x is None or x.dim() != 3:
+        raise ValueError("q or k [tokens, heads, dim] is needed")
+    if q is not None and k is not None and (
+            k.dim() != 3 or k.dtype is not q.dtype or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
+        raise ValueError("q and k must have the same type, tokens and head size")
+    code = _HALF_CODES.get(x.dtype)
+    if code is None:
+        code = dtype_code(x.dtype)
+    tokens, _, dim = x.shape
+    index, held = x.get_device(), []
+    _one_gpu(index, *(t for t in (q, k, positions, table, q_out, k_out) if t is not None))
+    if positions is not None and positions.shape != (tokens,):
+        raise ValueError("positions must have an entry for every token")
+    rows = rot = 0
+    if table is not None:
+        if table.dim() != 2 or not table.numel() or table.dtype is not _F32 or not table.is_contiguous():
+            raise ValueError("the table must be contiguous float32 [positions, rot_dim]")
+        rows, rot = table.shape
+    if q is not None:
+        q_out = _side(q, "q", q_weight, q_out, index, stream, held)
+    if k is not None:
+        k_out = _side(k, "k", k_weight, k_out, index, stream, held)
+    how = _NormRopeStruct(None if table is None else table.data_ptr(), rows, rot, interleaved, eps)
+    status = lib().w4_qk_norm_rope(
+        None if q is None else ctypes.addressof(held[0]),
+        None if k is None else ctypes.addressof(held[-1]), ctypes.addressof(how),
+        None if positions is None else _ints(positions, "positions"), tokens, dim, code,
+        _on(stream, index))
+    if status:
+        _check(status)
+    return q_out, k_out
 
 
 def w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len, q_heads, kv_heads,

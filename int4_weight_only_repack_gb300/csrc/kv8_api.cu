@@ -1,5 +1,5 @@
 // C ABI of the 8-bit key-value cache (the w4_kv8_* entry points of
-// include/w4a16.h): argument validation and dispatch. Every check runs on the
+// include/w4a16.h, and w4_qk_norm_rope before them): argument validation and dispatch. Every check runs on the
 // host before any CUDA call; nothing is launched on error. Table entries,
 // lengths and offsets live on the device and are checked by the kernels.
 #include <cuda_runtime.h>
@@ -108,9 +108,88 @@ bool any_alias(const Extent* e, int count, int writes) {
   return false;
 }
 
+// Whether two sides' rows share bytes: `tokens` rows of wa and wb bytes, sa and sb bytes
+// apart. Rows of one buffer (slices of a projection) lie at one stride and differ in
+// where they begin within it.
+bool rows_overlap(const void* a, size_t sa, size_t wa, const void* b, size_t sb, size_t wb, int tokens) {
+  const size_t last = (size_t)(tokens - 1);
+  if (!overlaps(a, last * sa + wa, b, last * sb + wb)) return false;
+  if (sa != sb) return true;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const size_t d = b0 >= a0 ? (b0 - a0) % sa : (sa - (a0 - b0) % sa) % sa;
+  return d < wa || d + wb > sa;
+}
+
+w4_status check_side(const w4_head_rows* r, int head_dim) {
+  if (r->heads < 1 || r->heads > MAX_HEADS || bad_stride(r->in_stride, r->heads * head_dim) ||
+      bad_stride(r->out_stride, r->heads * head_dim))
+    return W4_ERR_SHAPE;
+  if (!r->in || !r->out) return W4_ERR_NULL;
+  if (!aligned16(r->in) || !aligned16(r->out) || !aligned16(r->weight)) return W4_ERR_ALIGN;
+  return W4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+w4_status w4_qk_norm_rope(const w4_head_rows* q, const w4_head_rows* k, const w4_norm_rope* how,
+                          const int32_t* positions, int tokens, int head_dim, int dtype, void* stream) {
+  if (dtype != W4_F16 && dtype != W4_BF16) return W4_ERR_DTYPE;
+  if (!how) return W4_ERR_NULL;
+  if ((head_dim != 64 && head_dim != 128) || tokens < 0 || tokens > MAX_TOKENS || !(how->eps >= 0.f) ||
+      !std::isfinite(how->eps))
+    return W4_ERR_SHAPE;
+  const w4_head_rows* sides[2] = {q, k};
+  const bool turns = how->table != nullptr;
+  bool does = turns;
+  for (const w4_head_rows* s : sides) does = does || (s && s->weight);
+  if ((!q && !k) || !does) return W4_ERR_NULL;
+  if (turns && (how->rows < 1 || how->rot_dim < 16 || how->rot_dim > head_dim || how->rot_dim % 16 ||
+                how->interleaved < 0 || how->interleaved > 1))
+    return W4_ERR_SHAPE;
+  if (tokens == 0) return W4_OK;
+  w4_status st;
+  for (const w4_head_rows* s : sides)
+    if (s && (st = check_side(s, head_dim))) return st;
+  if (turns && !positions) return W4_ERR_NULL;
+  if (!aligned16(how->table) || !aligned4(positions)) return W4_ERR_ALIGN;
+  // an output shares no byte with anything else, but for its own input in place
+  const size_t table_b = turns ? (size_t)how->rows * how->rot_dim * 4 : 0;
+  for (const w4_head_rows* s : sides) {
+    if (!s) continue;
+    const size_t stride = s->out_stride * 2, width = (size_t)s->heads * head_dim * 2;
+    const size_t all = (size_t)(tokens - 1) * stride + width;
+    if (overlaps(s->out, all, how->table, table_b) || overlaps(s->out, all, positions, (size_t)tokens * 4))
+      return W4_ERR_ALIAS;
+    for (const w4_head_rows* o : sides) {
+      if (!o) continue;
+      const size_t wide = (size_t)o->heads * head_dim * 2;
+      if (overlaps(s->out, all, o->weight, (size_t)head_dim * 4)) return W4_ERR_ALIAS;
+      const bool in_place = o == s && s->out == s->in && s->out_stride == s->in_stride;
+      if (!in_place && rows_overlap(s->out, stride, width, o->in, o->in_stride * 2, wide, tokens)) return W4_ERR_ALIAS;
+      if (o != s && rows_overlap(s->out, stride, width, o->out, o->out_stride * 2, wide, tokens)) return W4_ERR_ALIAS;
+    }
+  }
+  if ((st = check_arch())) return st;
+  RopeArgs a = {};
+  for (int i = 0; i < 2; ++i)
+    if (const w4_head_rows* s = sides[i])
+      a.rows[i] = {static_cast<const uint16_t*>(s->in), static_cast<uint16_t*>(s->out), s->in_stride,
+                   s->out_stride, s->weight, s->heads};
+  if (turns) {
+    a.table = how->table;
+    a.table_rows = how->rows;
+    a.rot = how->rot_dim;
+    a.interleaved = how->interleaved;
+  }
+  a.positions = positions;
+  a.tokens = tokens;
+  a.dim = head_dim;
+  a.bf16 = dtype == W4_BF16;
+  a.eps = how->eps;
+  return from_cuda(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
 
 w4_status w4_kv8_append(const void* k_new, const void* v_new, size_t k_stride, size_t v_stride,
                         const w4_kv8_cache* cache, const int32_t* table,

@@ -21,6 +21,22 @@ struct Cache {
   int pages, page_shift, heads;  // page size = 1 << page_shift
 };
 
+struct HeadRows {  // a side of the norms and rotation; heads == 0: none
+  const uint16_t* in;
+  uint16_t* out;
+  size_t in_stride, out_stride;
+  const float* weight;
+  int heads;
+};
+struct RopeArgs {
+  HeadRows rows[2];
+  const float* table;
+  const int32_t* positions;
+  int table_rows, rot, interleaved, tokens, dim, bf16;
+  float eps;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
 struct AppendArgs {
   const uint16_t *k, *v;
   size_t k_stride, v_stride;

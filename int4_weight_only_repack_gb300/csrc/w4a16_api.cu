@@ -138,6 +138,7 @@ const char* w4_status_string(w4_status s) {
     case W4_ERR_PAGE: return "W4_ERR_PAGE: a page number, length or offset on the device is out of range";
     case W4_ERR_NO_PAGES: return "W4_ERR_NO_PAGES: too few free pages";
     case W4_ERR_SEQ: return "W4_ERR_SEQ: a sequence number is out of range, or a fork's target is not empty";
+    case W4_ERR_POSITION: return "W4_ERR_POSITION: a position on the device is past the table";
     default: return "unknown w4_status";
   }
 }
