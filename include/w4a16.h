@@ -545,6 +545,37 @@ W4_API w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_c
                                   const w4_kv8_heads* heads, int dtype, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* What the queries of a masked call see (a HOST struct, read during the call). */
+typedef struct w4_kv8_mask {
+    int window;           /* 0: no window; else 1 or more                            */
+    int sinks;            /* with a window: first tokens that stay visible, 0..2^30  */
+    const uint64_t* tree; /* [total_q] (device, 8-byte alignment), or NULL           */
+} w4_kv8_mask;
+
+/*
+ * w4_kv8_attention with heads->causal 1 and queries that see fewer tokens. Of sequence
+ * b's n = cu_q[b+1] - cu_q[b] queries the i-th sees
+ *   without a tree: the tokens j <= kv_lens[b] - n + i that lie in its window,
+ *       j > kv_lens[b] - n + i - window, or among the sinks, j < sinks;
+ *   with a tree: of the tokens before the new ones, j < kv_lens[b] - n, all; with a
+ *       window too, those with j >= kv_lens[b] - n + c - window, c the number of drafts
+ *       that it sees (its place in the sequence if they are its branch), or j < sinks;
+ *       and of the new ones, which are drafts, the d-th (token kv_lens[b] - n + d) where
+ *       bit d of tree[cu_q[b] + i] is set, whatever the window. Bit i is no exception, and
+ *       bits from n on mean nothing. max_q_len is 64 at most then (else W4_ERR_SHAPE).
+ * Codes and scales of tokens that no query of a sequence sees are not read, but for
+ * those near the others (within 256 tokens); their pages' numbers may be looked at.
+ * The workspace is that of w4_kv8_attention, as is everything else. A mask with neither
+ * window nor tree is W4_ERR_NULL; sinks without a window and causal 0 are W4_ERR_SHAPE.
+ */
+W4_API w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w4_kv8_cache* cache,
+                                         const int32_t* table, int table_stride,
+                                         const int32_t* kv_lens, const int32_t* cu_q, void* out,
+                                         int batch, int total_q, int max_q_len, int max_kv_len,
+                                         const w4_kv8_heads* heads, const w4_kv8_mask* mask,
+                                         int dtype, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 /*
  * The pages of a pool are counted by refs [num_pages] int32 (0: free), and its
  * sequences described by table [num_seqs][table_stride] and lens [num_seqs]

@@ -53,6 +53,11 @@ class _KV8HeadsStruct(ctypes.Structure):
     _fields_ = [("q_heads", _c_int), ("causal", _c_int), ("scale", ctypes.c_float)]
 
 
+class _KV8MaskStruct(ctypes.Structure):
+    """w4_kv8_mask."""
+    _fields_ = [("window", _c_int), ("sinks", _c_int), ("tree", _c_void_p)]
+
+
 class _HeadRowsStruct(ctypes.Structure):
     """w4_head_rows."""
     _fields_ = [("in_", _c_void_p), ("out", _c_void_p), ("in_stride", _c_size),
@@ -106,6 +111,10 @@ _SIGNATURES = {
     "w4_kv8_attention": (_c_int, [_c_void_p, _c_size, _c_void_p, _c_void_p, _c_int, _c_void_p,
                                   _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
                                   _c_void_p, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_attention_masked": (_c_int, [_c_void_p, _c_size, _c_void_p, _c_void_p, _c_int,
+                                         _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
+                                         _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_size,
+                                         _c_void_p]),
     "w4_kv8_pages_workspace_size": (_c_size, [_c_int, _c_int]),
     "w4_kv8_reserve": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int,
                                 _c_void_p, _c_int, _c_void_p, _c_void_p, _c_size, _c_void_p]),
@@ -707,13 +716,36 @@ def _space(nbytes, index, handle, stream):
     return got
 
 
+def _mask(window, sinks, tree, tokens, causal, index):
+    """The w4_kv8_mask of an attention call."""
+    if not causal:
+        raise ValueError("a window or a tree needs causal attention")
+    if window is not None and window < 1:
+        raise ValueError("the window must be 1 or more")
+    if sinks < 0 or (sinks and window is None):
+        raise ValueError("sinks are 0 or more, and need a window")
+    at = None
+    if tree is not None:
+        if tree.shape != (tokens,) or tree.dtype is not torch.int64 or not tree.is_contiguous():
+            raise ValueError("the tree must be contiguous int64, an entry for every token")
+        _one_gpu(index, tree)
+        at = tree.data_ptr()
+    return _KV8MaskStruct(min(window or 0, 2 ** 30), min(sinks, 2 ** 30), at)
+
+
 def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_len, scale=None,
-                  causal=True, out=None, workspace=None, stream=None):
+                  causal=True, out=None, workspace=None, stream=None, window=None, sinks=0,
+                  tree=None):
     """Attention of q [tokens, q_heads, head_dim] (fp16 or bf16, packed by
     sequence as for kv8_append) over each sequence's kv_lens[b] cached tokens;
     causal: its queries are its last tokens; otherwise each sees all of them.
     scale defaults to head_dim ** -0.5. Without `workspace`, the one kept for
-    (device, stream) is used. See w4_kv8_attention in include/w4a16.h."""
+    (device, stream) is used.
+    window: a query sees its own and the window - 1 tokens before it, and the first
+    `sinks` tokens. tree: int64 [tokens], the sequences' new tokens (64 at most each) are
+    a tree of drafts: bit d of a query's says that it sees its sequence's d-th draft (its
+    own is no exception); all that was there before the drafts it sees as without a tree.
+    Both need causal. See w4_kv8_attention and w4_kv8_attention_masked in include/w4a16.h."""
     shape, dtype, dim = q.shape, q.dtype, cache.head_dim
     tokens, heads = shape[0], shape[1]
     stride = _rows(q, "q", heads, dim)
@@ -726,6 +758,11 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     if out is not None and (out.shape != shape or out.dtype is not dtype or not out.is_contiguous()):
         raise ValueError("out must be contiguous, with q's shape and type")
     index = cache._device
+    mask = None
+    if window is not None or tree is not None:
+        mask = _mask(window, sinks, tree, tokens, causal, index)
+    elif sinks:
+        raise ValueError("sinks need a window")
     _one_gpu(index, q, q if out is None else out, table, kv_lens, cu_q)
     if out is None:
         out = _new(lambda: torch.empty_like(q, memory_format=torch.contiguous_format), stream, index)
@@ -750,10 +787,16 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     elif nbytes:
         space, nbytes = _space(nbytes, index, handle, stream)
     tab, tab_stride, held = _table(table, stream, index)
-    status = L.w4_kv8_attention(
-        q.data_ptr(), stride, cache._ref, tab, tab_stride, _ints(kv_lens, "kv_lens"),
-        _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len, max_kv_len, how[1], code,
-        space, nbytes, handle)
+    if mask is None:
+        status = L.w4_kv8_attention(
+            q.data_ptr(), stride, cache._ref, tab, tab_stride, _ints(kv_lens, "kv_lens"),
+            _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len, max_kv_len, how[1], code,
+            space, nbytes, handle)
+    else:
+        status = L.w4_kv8_attention_masked(
+            q.data_ptr(), stride, cache._ref, tab, tab_stride, _ints(kv_lens, "kv_lens"),
+            _ints(cu_q, "cu_q"), out.data_ptr(), batch, tokens, max_q_len, max_kv_len, how[1],
+            ctypes.addressof(mask), code, space, nbytes, handle)
     if status:
         _check(status)
     return out

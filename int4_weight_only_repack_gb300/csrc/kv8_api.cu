@@ -129,6 +129,67 @@ w4_status check_side(const w4_head_rows* r, int head_dim) {
   return W4_OK;
 }
 
+// Both attention calls.
+w4_status attend(const void* q, size_t q_stride, const w4_kv8_cache* cache, const int32_t* table,
+                 int table_stride, const int32_t* kv_lens, const int32_t* cu_q, void* out, int batch,
+                 int total_q, int max_q_len, int max_kv_len, const w4_kv8_heads* heads,
+                 const w4_kv8_mask& mask, int dtype, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  w4_status st = check_cache(cache);
+  if (st) return st;
+  if (!heads) return W4_ERR_NULL;
+  const int q_heads = heads->q_heads;
+  if ((st = check_batch(table, table_stride, kv_lens, cu_q, batch, total_q, max_q_len, dtype)))
+    return st;
+  if (q_heads < 1 || q_heads > MAX_HEADS || q_heads % cache->kv_heads || max_kv_len < 0 ||
+      max_kv_len > MAX_KV || heads->causal < 0 || heads->causal > 1 || !std::isfinite(heads->scale))
+    return W4_ERR_SHAPE;
+  const int width = q_heads * cache->head_dim;
+  if (bad_stride(q_stride, width)) return W4_ERR_SHAPE;
+  if (batch == 0 || total_q == 0 || max_q_len == 0) return W4_OK;
+  if (!q || !out) return W4_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return W4_ERR_ALIGN;
+  const size_t need = w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len,
+                                                      q_heads, cache->kv_heads, cache->head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
+  const size_t out_b = strided_bytes(total_q, width, width);
+  const Extent e[7] = {{out, out_b},
+                       {workspace, workspace ? need : 0},
+                       {q, strided_bytes(total_q, q_stride, width)},
+                       {table, table_bytes(batch, table_stride)},
+                       {kv_lens, (size_t)batch * 4},
+                       {cu_q, (size_t)(batch + 1) * 4},
+                       {mask.tree, (size_t)total_q * 8}};
+  if (any_alias(e, 7, 2) || overlaps_cache(cache, out, out_b) ||
+      overlaps_cache(cache, workspace, workspace ? need : 0))
+    return W4_ERR_ALIAS;
+  if ((st = check_arch())) return st;
+  AttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.c = device_cache(cache);
+  a.table = table;
+  a.kv_lens = kv_lens;
+  a.cu_q = cu_q;
+  a.out = static_cast<uint16_t*>(out);
+  a.table_stride = table_stride;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.max_q = max_q_len;
+  a.max_kv = max_kv_len;
+  a.q_heads = q_heads;
+  a.dim = cache->head_dim;
+  a.causal = heads->causal;
+  a.bf16 = dtype == W4_BF16;
+  a.scale = heads->scale;
+  a.workspace = workspace;
+  a.window = mask.window;
+  a.sinks = mask.sinks;
+  a.tree = mask.tree;
+  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
+  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -243,55 +304,24 @@ w4_status w4_kv8_attention(const void* q, size_t q_stride, const w4_kv8_cache* c
                            const int32_t* cu_q, void* out, int batch, int total_q, int max_q_len,
                            int max_kv_len, const w4_kv8_heads* heads, int dtype, void* workspace,
                            size_t workspace_bytes, void* stream) {
-  w4_status st = check_cache(cache);
-  if (st) return st;
-  if (!heads) return W4_ERR_NULL;
-  const int q_heads = heads->q_heads;
-  if ((st = check_batch(table, table_stride, kv_lens, cu_q, batch, total_q, max_q_len, dtype)))
-    return st;
-  if (q_heads < 1 || q_heads > MAX_HEADS || q_heads % cache->kv_heads || max_kv_len < 0 ||
-      max_kv_len > MAX_KV || heads->causal < 0 || heads->causal > 1 || !std::isfinite(heads->scale))
+  const w4_kv8_mask none = {0, 0, nullptr};
+  return attend(q, q_stride, cache, table, table_stride, kv_lens, cu_q, out, batch, total_q, max_q_len,
+                max_kv_len, heads, none, dtype, workspace, workspace_bytes, stream);
+}
+
+w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w4_kv8_cache* cache,
+                                  const int32_t* table, int table_stride, const int32_t* kv_lens,
+                                  const int32_t* cu_q, void* out, int batch, int total_q,
+                                  int max_q_len, int max_kv_len, const w4_kv8_heads* heads,
+                                  const w4_kv8_mask* mask, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!mask || (mask->window == 0 && !mask->tree)) return W4_ERR_NULL;
+  if (mask->window < 0 || mask->sinks < 0 || mask->sinks > MAX_KV || (mask->sinks > 0 && mask->window == 0) ||
+      (heads && heads->causal != 1) || (mask->tree && max_q_len > MAX_DRAFTS))
     return W4_ERR_SHAPE;
-  const int width = q_heads * cache->head_dim;
-  if (bad_stride(q_stride, width)) return W4_ERR_SHAPE;
-  if (batch == 0 || total_q == 0 || max_q_len == 0) return W4_OK;
-  if (!q || !out) return W4_ERR_NULL;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return W4_ERR_ALIGN;
-  const size_t need = w4_kv8_attention_workspace_size(batch, total_q, max_q_len, max_kv_len,
-                                                      q_heads, cache->kv_heads, cache->head_dim);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
-  const size_t out_b = strided_bytes(total_q, width, width);
-  const Extent e[6] = {{out, out_b},
-                       {workspace, workspace ? need : 0},
-                       {q, strided_bytes(total_q, q_stride, width)},
-                       {table, table_bytes(batch, table_stride)},
-                       {kv_lens, (size_t)batch * 4},
-                       {cu_q, (size_t)(batch + 1) * 4}};
-  if (any_alias(e, 6, 2) || overlaps_cache(cache, out, out_b) ||
-      overlaps_cache(cache, workspace, workspace ? need : 0))
-    return W4_ERR_ALIAS;
-  if ((st = check_arch())) return st;
-  AttnArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
-  a.c = device_cache(cache);
-  a.table = table;
-  a.kv_lens = kv_lens;
-  a.cu_q = cu_q;
-  a.out = static_cast<uint16_t*>(out);
-  a.table_stride = table_stride;
-  a.batch = batch;
-  a.total_q = total_q;
-  a.max_q = max_q_len;
-  a.max_kv = max_kv_len;
-  a.q_heads = q_heads;
-  a.dim = cache->head_dim;
-  a.causal = heads->causal;
-  a.bf16 = dtype == W4_BF16;
-  a.scale = heads->scale;
-  a.workspace = workspace;
-  const std::lock_guard<std::mutex> lock(stream_mutex(stream));
-  return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
+  if (reinterpret_cast<uintptr_t>(mask->tree) & 7u) return W4_ERR_ALIGN;
+  return attend(q, q_stride, cache, table, table_stride, kv_lens, cu_q, out, batch, total_q, max_q_len,
+                max_kv_len, heads, *mask, dtype, workspace, workspace_bytes, stream);
 }
 
 size_t w4_kv8_pages_workspace_size(int num_pages, int n) {

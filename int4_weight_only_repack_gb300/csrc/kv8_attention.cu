@@ -62,7 +62,7 @@ struct Rows {
   Attn a;
   float* part;  // [warp][2]: sums [rows][D], then maximum and l [rows][2]
   int* rec;     // [warp][8]: the item begun but not finished there (Begun)
-  int row_tiles, split, bf16;
+  int row_tiles, split, bf16, mask;
 };
 
 __host__ __device__ constexpr int part_floats(int D, int NB) { return 8 * NB * (D + 2); }
@@ -74,22 +74,35 @@ struct alignas(32) Begun {
   int q0, rows, h, tile;
 };
 
-// A run of units [u0, u1) of one item.
+// A run of units [u0, u1) of one item. A masked item's units are those of the sinks and
+// those from its first row's window on, counted through.
 struct Seg {
   int b, h, tile, tiles, units, u0, u1;
+  int sink_units, skip;  // of a masked call
   Seq s;
   long long left;  // cost of the run from this item's part on
 };
 
-template <int ROWS>
+template <int ROWS, bool MASK>
 __device__ __forceinline__ void count_items(const Attn& a, Seg& g) {
   g.tiles = (g.s.n * a.group + ROWS - 1) / ROWS;
   g.units = max(1, (g.s.kv + STEP - 1) / STEP);
+  if constexpr (MASK) {  // (the same for all tiles: a sequence has at most 64 tokens here)
+    g.sink_units = (int)(((long long)a.sinks + STEP - 1) / STEP);
+    g.skip = max(0, first_seen(a, g.s, 0) / STEP - g.sink_units);
+    g.units = max(1, g.units - g.skip);
+  }
 }
-template <int ROWS>
+template <int ROWS, bool MASK>
 __device__ __forceinline__ void load_items(const Attn& a, Seg& g) {
   g.s = load_seq(a, g.b);
-  count_items<ROWS>(a, g);
+  count_items<ROWS, MASK>(a, g);
+}
+// The first token of unit u.
+template <bool MASK>
+__device__ __forceinline__ int token_of(const Seg& g, int u) {
+  if constexpr (MASK) return (u < g.sink_units ? u : u + g.skip) * STEP;
+  else return u * STEP;
 }
 
 // The item's part of a run that begins `skip` into its cost.
@@ -100,7 +113,7 @@ __device__ __forceinline__ void cut(Seg& g, long long skip) {
 }
 
 // The next part with a unit in it; false at the run's end.
-template <int ROWS>
+template <int ROWS, bool MASK>
 __device__ __forceinline__ bool next_seg(const Attn& a, Seg& g) {
   if (g.left <= ITEM_COST) return false;
   if (++g.tile >= g.tiles) {
@@ -109,7 +122,7 @@ __device__ __forceinline__ bool next_seg(const Attn& a, Seg& g) {
       g.h = 0;
       do {
         if (++g.b >= a.batch) return false;
-        load_items<ROWS>(a, g);
+        load_items<ROWS, MASK>(a, g);
       } while (g.tiles == 0);
     }
   }
@@ -154,7 +167,11 @@ struct Layout {
   static_assert(WARPS * ROWS * OS * 4 <= WARPS * RING, "the merge buffer takes the place of the rings");
   static constexpr int OFF_BAR = OFF_SC + WARPS * STAGES * 16;
   static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
-  static constexpr int BYTES = OFF_MISC + 8 + WARPS * 32 + 1024;  // + slack to align the base
+  static constexpr int OFF_SEES = OFF_MISC + 8 + WARPS * 32 + 8;  // a masked call's [warp][row]
+  static constexpr int bytes(bool mask) {  // + slack to align the base
+    return (mask ? OFF_SEES + WARPS * ROWS * 16 : OFF_MISC + 8 + WARPS * 32) + 1024;
+  }
+  static_assert(OFF_SEES % 16 == 0, "masks are read in pieces of 16 bytes");
 };
 
 // The queries of an item, one row a lane (its operand's column): row 8 nb + g.
@@ -184,8 +201,14 @@ __device__ __forceinline__ uint16_t* out_row(const Attn& a, const Seg& g, int rr
   return a.out + ((size_t)(g.s.q0 + tok) * a.q_heads + g.h * a.group + (rr - tok * a.group)) * D;
 }
 
-// SPLIT: every warp has a run of its own; otherwise a CTA has an item.
-template <int D, int NB, bool BF16, bool SPLIT>
+// SPLIT: every warp has a run of its own; otherwise a CTA has an item. MASK: a window or
+// a tree; what a row sees then stands in shared memory (in registers, as without one, it
+// would spill), its bits for the new tokens and a bound for those before.
+struct alignas(16) Sees {
+  uint64_t drafts;  // bit i: new token i of the sequence
+  int lo, pad;
+};
+template <int D, int NB, bool BF16, bool SPLIT, bool MASK>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid_constant__ Rows r) {
   using L = Layout<D, NB>;
   constexpr int ROWS = L::ROWS;
@@ -203,6 +226,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
   float* sc_sh = reinterpret_cast<float*>(smem + L::OFF_SC) + warp * STAGES * 4;
   const uint32_t bars = smem_addr(smem + L::OFF_BAR) + warp * STAGES * 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
+  Sees* sees_sh = reinterpret_cast<Sees*>(smem + L::OFF_SEES) + warp * ROWS;
 
   if (lane == 0) {
     // arrivals: TMA, and two scales for each page of a unit
@@ -226,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     seg.tile = blockIdx.x - bh * r.row_tiles;
     seg.b = bh / a.c.heads;
     seg.h = bh - seg.b * a.c.heads;
-    load_items<ROWS>(a, seg);
+    load_items<ROWS, MASK>(a, seg);
     if (!seg.s.ok && threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
     if (seg.s.n > a.max_q) {
       zero_rows<D>(a, seg.s, seg.h, seg.tile, r.row_tiles);
@@ -246,7 +270,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     const int b0 = min(a.batch, (int)threadIdx.x * per_t), b1 = min(a.batch, b0 + per_t);
     long long sum = 0;
     for (seg.b = b0; seg.b < b1; ++seg.b) {
-      load_items<ROWS>(a, seg);
+      load_items<ROWS, MASK>(a, seg);
       if (!seg.s.ok && blockIdx.x == 0) record(a.status, W4_ERR_PAGE);
       sum += (long long)seg.tiles * a.c.heads * (ITEM_COST + seg.units);
     }
@@ -273,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
       for (int b = b0; b < b1; ++b) {
         if (per_t > 1) {
           seg.b = b;
-          load_items<ROWS>(a, seg);
+          load_items<ROWS, MASK>(a, seg);
         }
         const long long n = (long long)seg.tiles * a.c.heads * (ITEM_COST + seg.units);
         if (lo < at + n) {
@@ -291,13 +315,13 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     if (any) {
       seg.b = seqs[4 * warp];
       seg.s = {seqs[4 * warp + 1], seqs[4 * warp + 2], seqs[4 * warp + 3], true};
-      count_items<ROWS>(a, seg);
+      count_items<ROWS, MASK>(a, seg);
       const int item = (int)(runs[warp] / (ITEM_COST + seg.units));
       seg.h = item / seg.tiles;
       seg.tile = item - seg.h * seg.tiles;
       seg.left = min(per, total - lo);
       cut(seg, runs[warp] - (long long)item * (ITEM_COST + seg.units));
-      while (any && seg.u0 >= seg.u1) any = next_seg<ROWS>(a, seg);  // only its begin lies here
+      while (any && seg.u0 >= seg.u1) any = next_seg<ROWS, MASK>(a, seg);  // only its begin lies here
     }
   }
   constexpr int STRIDE = SPLIT ? 1 : WARPS;
@@ -313,14 +337,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
   bool more = any, ok = true;
   auto settle = [&]() {  // move to the next segment with a unit for this warp; fetch its pages
     while (pu >= ps.u1) {
-      if (!next_seg<ROWS>(a, ps)) {
+      if (!next_seg<ROWS, MASK>(a, ps)) {
         more = false;
         return;
       }
       pu = ps.u0 + phase;
     }
     if (lane < 2) {
-      const int j = pu * STEP + 16 * lane;
+      const int j = token_of<MASK>(ps, pu) + 16 * lane;
       page_reg = j < ps.s.kv ? a.table[(size_t)ps.b * a.table_stride + (j >> shift)] : -2;
     }
   };
@@ -340,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
       const uint32_t box = halves ? HALF : L::TILE;
       mbar_arrive_expect_tx(bar, (p0 >= 0 ? 2 * box : 0) + (p1 >= 0 ? 2 * box : 0));
       if (p0 >= 0) {
-        const int y = (p0 << shift) + ((pu * STEP) & ((1 << shift) - 1));
+        const int y = (p0 << shift) + (token_of<MASK>(ps, pu) & ((1 << shift) - 1));
         tma_load_2d(dst, &r.tk, bar, 0, y);
         tma_load_2d(dst + L::TILE, &r.tv, bar, 0, y);
       }
@@ -396,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
   };
   for (bool go = any; go;) {
     Seg nxt = seg;
-    go = next_seg<ROWS>(a, nxt);
+    go = next_seg<ROWS, MASK>(a, nxt);
     const Seq s = seg.s;
     const int rows = s.n * a.group, row0 = seg.tile * ROWS;
     // queries as fp16 scaled to [2^14, 2^15): lane (g, t) loads row 8 nb + g (its
@@ -404,12 +428,21 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
     uint32_t qf[NB][MT][2];
     float fr[NB][2];
     int lim[NB][2];
+    if constexpr (MASK) __syncwarp();  // the last item's masks have been read
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = row0 + 8 * nb + g;
       const bool real = row < rows;
       const int tok = real ? row / a.group : 0;
       const int sees = !real ? 0 : a.causal ? min(s.kv, s.kv - s.n + tok + 1) : s.kv;
+      if constexpr (MASK) {
+        if (t == 0) {
+          const Sight y = sight_of(a, s, tok);
+          const int base = s.kv - s.n;
+          const uint64_t drafts = a.tree ? y.bits : below64(tok + 1) & (~below64(y.lo - base) | below64(a.sinks - base));
+          sees_sh[8 * nb + g] = {real ? drafts : 0, real ? y.lo : MAX_KV, 0};
+        }
+      }
       float f[CH][16];
       float amax = 0.f;
 #pragma unroll
@@ -445,7 +478,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
       }
     }
     if (go) qr.load(a, nxt, g, t);
-    const int first_lim = a.causal ? min(s.kv, s.kv - s.n + row0 / a.group + 1) : s.kv;
+    if constexpr (MASK) __syncwarp();
+    const int first_lim = MASK ? s.kv - s.n : a.causal ? min(s.kv, s.kv - s.n + row0 / a.group + 1) : s.kv;
+    const int all_lo = MASK ? all_see_from(a, s, s.n - 1) : 0;
 
     // The base m of the exponents is a row's maximum when it was last raised: it is
     // raised only when a score passes it by more than P_ROOM, so most units exchange
@@ -460,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
       for (int i = 0; i < MT; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
     }
     for (int u = seg.u0 + phase; u < seg.u1; u += STRIDE) {
-      const int st = it % STAGES, j0 = u * STEP;
+      const int st = it % STAGES, j0 = token_of<MASK>(seg, u);
       if (ok) ok = __all_sync(~0u, wait_for(bars + 8 * st, (it / STAGES) & 1, abort_flag, a.status));
       if (!ok) break;
       ++it;
@@ -522,7 +557,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
             x[nb][half][2 + i] = x[nb][half][2 + i] * f + c;
           }
       }
-      if (j0 + STEP > first_lim || ksc[0] == NEG_INF || ksc[1] == NEG_INF) {
+      if (j0 + STEP > first_lim || (MASK && j0 < all_lo && j0 + STEP > a.sinks) || ksc[0] == NEG_INF ||
+          ksc[1] == NEG_INF) {
         // Some row does not see every token. Slots that hold none leave the value
         // operand. So do NaN codes, since 0 * NaN is NaN: they come back through the
         // scores of the rows that see them.
@@ -540,17 +576,34 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) rows_kernel(const __grid
             }
           }
         nan_tokens = __reduce_or_sync(~0u, nan_tokens);
+        if constexpr (MASK) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float& y = x[nb][n >> 1][2 * (n & 1) + i];
-              const int col = 8 * n + rho(g);
-              if (nan_tokens >> col & 1) y = __int_as_float(0x7FFFFFFF);
-              if (j0 + col >= lim[nb][i] || ksc[n >> 1] == NEG_INF) y = NEG_INF;
+              const Sees see = sees_sh[8 * nb + 2 * t + i];
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                float& y = x[nb][n >> 1][2 * (n & 1) + i];
+                const int col = 8 * n + rho(g), j = j0 + col, d = j - first_lim;
+                if (nan_tokens >> col & 1) y = __int_as_float(0x7FFFFFFF);
+                const bool seen = d < 0 ? j >= see.lo || j < a.sinks : d < MAX_DRAFTS && (see.drafts >> d & 1);
+                if (!seen || ksc[n >> 1] == NEG_INF) y = NEG_INF;
+              }
             }
+        } else {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float& y = x[nb][n >> 1][2 * (n & 1) + i];
+                const int col = 8 * n + rho(g);
+                if (nan_tokens >> col & 1) y = __int_as_float(0x7FFFFFFF);
+                if (j0 + col >= lim[nb][i] || ksc[n >> 1] == NEG_INF) y = NEG_INF;
+              }
+        }
       }
       float top[NB][2];
       bool over = false;
@@ -871,32 +924,37 @@ bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX
 // Rows of queries that share one widening of the codes, in eights.
 int row_blocks(long long rows) { return rows > 8 ? 2 : 1; }
 
-template <int D, int NB, bool BF16>
+template <int D, int NB, bool BF16, bool MASK>
 cudaError_t launch_rows(Rows& r, int sms, cudaStream_t s) {
   static bool done[2][64] = {};
   const long long rows = (long long)r.a.max_q * r.a.group;
   const long long tiles = (rows + 8 * NB - 1) / (8 * NB), items = tiles * r.a.c.heads * r.a.batch;
   cudaError_t e;
   if (!r.split) {
-    constexpr int bytes = Layout<D, NB>::BYTES;
+    constexpr int bytes = Layout<D, NB>::bytes(MASK);
     if (items >= (1ll << 31)) return cudaErrorInvalidValue;
     r.row_tiles = (int)tiles;
-    if ((e = allow_smem(rows_kernel<D, NB, BF16, false>, bytes, done[0])) != cudaSuccess) return e;
-    return launch(rows_kernel<D, NB, BF16, false>, dim3((unsigned)items), THREADS, bytes, s, r);
+    if ((e = allow_smem(rows_kernel<D, NB, BF16, false, MASK>, bytes, done[0])) != cudaSuccess) return e;
+    return launch(rows_kernel<D, NB, BF16, false, MASK>, dim3((unsigned)items), THREADS, bytes, s, r);
   }
-  constexpr int bytes = Layout<D, NB>::BYTES;
-  if ((e = allow_smem(rows_kernel<D, NB, BF16, true>, bytes, done[1])) != cudaSuccess) return e;
+  constexpr int bytes = Layout<D, NB>::bytes(MASK);
+  if ((e = allow_smem(rows_kernel<D, NB, BF16, true, MASK>, bytes, done[1])) != cudaSuccess) return e;
   const int grid = std::min(sms, MAX_SMS) * CTAS_PER_SM;
-  if ((e = launch(rows_kernel<D, NB, BF16, true>, dim3(grid), THREADS, bytes, s, r)) != cudaSuccess) return e;
+  if ((e = launch(rows_kernel<D, NB, BF16, true, MASK>, dim3(grid), THREADS, bytes, s, r)) != cudaSuccess) return e;
   return launch(join_kernel<D, NB, BF16>, dim3(grid, (unsigned)std::min<long long>(8 * NB, rows)), THREADS, 0,
                 s, r);
+}
+
+template <int D, int NB, bool BF16>
+cudaError_t launch_mask(Rows& r, int sms, cudaStream_t s) {
+  return r.mask ? launch_rows<D, NB, BF16, true>(r, sms, s) : launch_rows<D, NB, BF16, false>(r, sms, s);
 }
 
 template <int D>
 cudaError_t launch_d(Rows& r, int sms, cudaStream_t s) {
   if (row_blocks((long long)r.a.max_q * r.a.group) == 1)
-    return r.bf16 ? launch_rows<D, 1, true>(r, sms, s) : launch_rows<D, 1, false>(r, sms, s);
-  return r.bf16 ? launch_rows<D, 2, true>(r, sms, s) : launch_rows<D, 2, false>(r, sms, s);
+    return r.bf16 ? launch_mask<D, 1, true>(r, sms, s) : launch_mask<D, 1, false>(r, sms, s);
+  return r.bf16 ? launch_mask<D, 2, true>(r, sms, s) : launch_mask<D, 2, false>(r, sms, s);
 }
 
 }  // namespace
@@ -933,12 +991,14 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s) {
   Rows r;
   r.a = {a.q, a.q_stride, a.c, a.table, a.kv_lens, a.cu_q, a.out, a.table_stride, a.batch,
          a.total_q, a.max_q, a.max_kv, a.q_heads, a.q_heads / a.c.heads, a.causal,
-         a.scale * 1.44269504088896340736f, status};
-  if (many_rows(a.max_q, r.a.group)) return launch_prompt(r.a, a.dim, a.bf16, a.workspace, s);
+         a.scale * 1.44269504088896340736f, status, a.window > 0 ? std::min(a.window, NO_WINDOW) : NO_WINDOW,
+         a.sinks, a.tree};
+  r.mask = a.window > 0 || a.tree;
+  if (many_rows(a.max_q, r.a.group)) return launch_prompt(r.a, a.dim, a.bf16, r.mask, a.workspace, s);
   const int box = std::min(1 << a.c.page_shift, STEP);
   if (!encode_rows(&r.tk, a.c.k, a.c, a.dim, box) || !encode_rows(&r.tv, a.c.v, a.c, a.dim, box))
     return cudaErrorInvalidValue;
-  r.split = splits(a.batch, a.max_kv);
+  r.split = splits(a.batch, (int)seen_at_most(r.a, r.a.max_q));
   r.bf16 = a.bf16;
   r.rec = static_cast<int*>(a.workspace);
   r.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + MAX_WORKERS * sizeof(Begun));

@@ -19,9 +19,16 @@
 // raising the base means rescaling O: a prompt of 8000 tokens took 448 us with P_ROOM
 // 4, 434 with 5, 427 with 6, 418 with 7, 414 with 8 (P_UP = 15 - P_ROOM, 10 for 4).
 //
+// A masked call (a window with sinks, a tree of drafts) computes the same over fewer
+// tokens: what no row of an item sees is not read (all but the sinks before the first
+// row's window), and of the rest a row's scores of tokens that it does not see become
+// -inf, in the steps where some row does not see all.
+//
 // The q_heads / kv_heads query heads that share a kv head, and the new tokens
 // of a sequence, are rows of one item: row r is token r / group, head r % group.
 #pragma once
+
+#include <algorithm>
 
 #include "decode_common.cuh"
 #include "kv8_device.cuh"
@@ -63,14 +70,22 @@ struct Attn {
   int table_stride, batch, total_q, max_q, max_kv, q_heads, group, causal;
   float scale_log2;  // scale * log2(e)
   int* status;
+  int window, sinks;     // of a masked call; window NO_WINDOW: none
+  const uint64_t* tree;  // or nullptr
 };
+constexpr int NO_WINDOW = MAX_KV;  // every token is as near
 
 // A tensor map over one side's token rows, a box `rows` of them high.
 bool encode_rows(CUtensorMap* map, const void* base, const Cache& c, int D, int rows);
 
 // The kernel for many rows (kv8_prompt.cu).
-cudaError_t launch_prompt(const Attn& a, int dim, int bf16, void* workspace, cudaStream_t s);
+cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* workspace, cudaStream_t s);
 size_t prompt_workspace_bytes(int batch, int max_q, int max_kv, int group, int kv_heads, int dim);
+
+// The most tokens that `queries` neighbouring ones see between them.
+inline long long seen_at_most(const Attn& a, long long queries) {
+  return std::min<long long>(a.max_kv, (long long)a.sinks + a.window + queries);
+}
 
 template <bool BF16>
 __device__ __forceinline__ float to_float(uint16_t h) {
@@ -132,6 +147,31 @@ __device__ __forceinline__ Seq load_seq(const Attn& a, int b) {
     s.ok = false;
   }
   return s;
+}
+
+// The lowest n of 32 or 64 bits, n of any sign.
+__device__ __forceinline__ uint32_t below32(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+__device__ __forceinline__ uint64_t below64(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// What query `tok` of a sequence of a masked call sees: the tokens before `lim` from `lo`
+// on or among the sinks, and with a tree the drafts (tokens kv - n and on) of its bits.
+struct Sight {
+  int lo, lim;
+  uint64_t bits;
+};
+__device__ __forceinline__ Sight sight_of(const Attn& a, const Seq& s, int tok) {
+  const int base = s.kv - s.n;
+  if (!a.tree) return {base + tok + 1 - a.window, min(s.kv, base + tok + 1), 0};
+  const uint64_t bits = a.tree[s.q0 + tok] & below64(s.n);
+  return {base + __popcll(bits) - a.window, base, bits};
+}
+// The first token that some query from `tok` on may see beside the sinks, and the one
+// from which on all up to query `last` see every token before base.
+__device__ __forceinline__ int first_seen(const Attn& a, const Seq& s, int tok) {
+  return max(0, s.kv - s.n + (a.tree ? 0 : tok + 1) - a.window);
+}
+__device__ __forceinline__ int all_see_from(const Attn& a, const Seq& s, int last) {
+  return s.kv - s.n + (a.tree ? s.n : last + 1) - a.window;
 }
 
 // Zeros to all rows of a sequence in the query heads of kv head h: a block's share.

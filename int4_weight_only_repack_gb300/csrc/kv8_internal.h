@@ -13,6 +13,7 @@ constexpr int MAX_BATCH = 1 << 20;
 constexpr int MAX_TOKENS = 1 << 24;  // new tokens of a call
 constexpr int MAX_KV = 1 << 30;      // tokens that a sequence holds
 constexpr int MAX_HEADS = 1024;
+constexpr int MAX_DRAFTS = 64;       // of a sequence: the bits of a tree's words
 
 // What the kernels need of a cache: pages as rows of head_dim bytes.
 struct Cache {
@@ -55,6 +56,8 @@ struct AttnArgs {
   int table_stride, batch, total_q, max_q, max_kv, q_heads, dim, causal, bf16;
   float scale;
   void* workspace;
+  int window, sinks;     // window 0: none
+  const uint64_t* tree;  // or nullptr
 };
 size_t attention_workspace_bytes(int batch, int max_q, int max_kv, int q_heads, int kv_heads,
                                  int dim);

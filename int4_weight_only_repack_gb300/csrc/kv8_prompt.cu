@@ -74,7 +74,7 @@ struct Prompt {
   CUtensorMap tk, tv;  // token rows [pages * heads * page][D] bytes, box of a page
   int tiles;           // of the longest sequence, of CTA_ROWS rows
   int parts;           // of an item
-  int bf16;
+  int bf16, mask;
   float* sums;         // with parts > 1: [item][part][CTA_ROWS][D + 2], sums, maximum, l
 };
 
@@ -229,7 +229,7 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, int GS, bool SPLIT>
+template <int D, int GS, bool SPLIT, bool MASK>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Prompt p) {
   using L = PLayout<D, GS>;
   constexpr int NB = L::NB, SB = L::SB;
@@ -265,15 +265,31 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     const int first = row0 + TILE_ROWS * i;
     if (first >= rows) return 0;
     const int tok = (min(rows, first + TILE_ROWS) - 1) / a.group;
-    return a.causal ? max(0, min(s.kv, s.kv - s.n + tok + 1)) : s.kv;
+    return a.causal && !(MASK && a.tree) ? max(0, min(s.kv, s.kv - s.n + tok + 1)) : s.kv;
   };
-  // this part's: steps0 and steps1 of them from token k0 on
-  const int all0 = (tokens_of(0) + KT - 1) / KT, all1 = (tokens_of(1) + KT - 1) / KT;
+  // a masked item's steps: those of the sinks, and those from its first row's window on
+  const int first_tok = row0 / a.group, last_tok = (min(rows, row0 + CTA_ROWS) - 1) / a.group;
+  const int sink_steps = MASK ? (int)(((long long)a.sinks + KT - 1) / KT) : 0;
+  const int skip = MASK ? max(0, first_seen(a, s, first_tok) / KT - sink_steps) : 0;
+  auto steps_of = [&](int tokens) {
+    const int all = (tokens + KT - 1) / KT;
+    return MASK && all > sink_steps ? max(sink_steps, all - skip) : all;
+  };
+  // this part's: steps0 and steps1 of them from step j0 on
+  const int all0 = steps_of(tokens_of(0)), all1 = steps_of(tokens_of(1));
   const int per = (max(all0, all1) + parts - 1) / parts, j0 = part * per, k0 = KT * j0;
   const int steps0 = max(0, min(all0 - j0, per)), steps1 = max(0, min(all1 - j0, per));
   const int steps = max(steps0, steps1);
-  // tokens from which on some row of the CTA does not see all
-  const int first_lim = a.causal ? max(0, min(s.kv, s.kv - s.n + row0 / a.group + 1)) : s.kv;
+  auto token_of = [&](int j) {  // the first of the part's step j
+    if constexpr (MASK) return KT * (j0 + j < sink_steps ? j0 + j : j0 + j + skip);
+    else return k0 + KT * j;
+  };
+  // tokens from which on some row of the CTA does not see all; and, masked, until which
+  const int first_lim = a.causal ? max(0, min(s.kv, s.kv - s.n + (MASK && a.tree ? 0 : first_tok + 1))) : s.kv;
+  const int all_lo = MASK ? all_see_from(a, s, last_tok) : 0;
+  auto partly_seen = [&](int t) {  // of the step from token t on
+    return t + KT > first_lim || (MASK && t < all_lo && t + KT > a.sinks);
+  };
 
   // For the warp that brings codes in: lane g < 8 has the step's sixteen g, its page's
   // number, read two steps ahead; the first lane of a page has its copies, the first
@@ -284,11 +300,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   const bool scales = lane < 8 && (16 * g) % GS == 0;
   const uint32_t page_bytes = (uint32_t)D << shift;
   auto page_at = [&](int j) {
-    const int t = k0 + KT * j + 16 * g;
+    const int t = token_of(j) + 16 * g;
     return j < steps && t < s.kv ? table[t >> shift] : -1;
   };
   auto row_of = [&](int j, int pg) {  // page and head; -1: no page
-    const bool real = j < steps && k0 + KT * j + 16 * g < s.kv;
+    const bool real = j < steps && token_of(j) + 16 * g < s.kv;
     if (real && (unsigned)pg >= (unsigned)a.c.pages) record(a.status, W4_ERR_PAGE);
     return real && (unsigned)pg < (unsigned)a.c.pages ? pg * a.c.heads + h : -1;
   };
@@ -337,7 +353,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     const int lrow = quarter * 32 + lane, row = row0 + TILE_ROWS * i + lrow;
     const bool real = row < rows;
     const int tok = real ? row / a.group : 0;
-    const int lim = !real ? 0 : a.causal ? min(s.kv, s.kv - s.n + tok + 1) : s.kv;
+    Sight sees = {0, !real ? 0 : a.causal ? min(s.kv, s.kv - s.n + tok + 1) : s.kv, 0};
+    if constexpr (MASK)
+      if (real) sees = sight_of(a, s, tok);
     const int my_steps = i ? steps1 : steps0;
     float fr;
     {
@@ -388,16 +406,23 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, x[c]);
       const float4* sc = reinterpret_cast<const float4*>(smem + L::OFF_SC) + (j % SLOTS) * SB;
       tmem_ld_wait();
-      if (k0 + KT * j + KT > first_lim) {  // some row does not see every token
+      const int t0 = token_of(j);
+      if (partly_seen(t0)) {  // some row does not see every token
         const uint32_t* nan = reinterpret_cast<const uint32_t*>(smem + L::OFF_NAN) + (j % SLOTS) * 4;
-        const int left = lim - k0 - KT * j;
+        const int left = sees.lim - t0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t bad = nan[c];
+          uint32_t seen = 0;  // tokens of the 32
+          if constexpr (MASK) {
+            const int t = t0 + 32 * c, d = t - s.kv + s.n;  // d: the draft that it begins with
+            seen = below32(sees.lim - t) & (~below32(sees.lo - t) | below32(a.sinks - t));
+            if (d > -32 && d < MAX_DRAFTS) seen |= (uint32_t)(d < 0 ? sees.bits << -d : sees.bits >> d);
+          }
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             if (bad >> k & 1) x[c][k] = 0x7FFFFFFFu;
-            if (32 * c + k >= left) x[c][k] = __float_as_uint(NEG_INF);
+            if (MASK ? !(seen >> k & 1) : 32 * c + k >= left) x[c][k] = __float_as_uint(NEG_INF);
           }
         }
       }
@@ -567,16 +592,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     // tokens of the step that are none (of a page that does not exist, or past the end)
     auto absent = [&](int j, int slot, int i) {
       const int r = 32 * i + r32;
-      return !(in[slot] >> (r >> 4) & 1) || k0 + KT * j + r >= s.kv;
+      return !(in[slot] >> (r >> 4) & 1) || token_of(j) + r >= s.kv;
     };
     auto wait_warp = [&](uint32_t bar, uint32_t ph) { return __all_sync(~0u, wait_for(bar, ph, abort_flag, a.status)); };
     for (int j = 0; j < steps; ++j) {
       const int stage = j % KV_STAGES, slot = j % SLOTS;
       const uint32_t ph = ((j / KV_STAGES) & 1) ^ 1;
-      const bool edge = k0 + KT * j + KT > first_lim;
+      const bool edge = partly_seen(token_of(j));
       if (!wait_warp(bars.rawfull(0), j & 1)) break;
       take(L::OFF_RK);
-      const bool part = k0 + KT * j + KT > s.kv || in[slot] != 0xFFu;
+      const bool part = token_of(j) + KT > s.kv || in[slot] != 0xFFu;
       if (part) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -784,17 +809,17 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
     *reinterpret_cast<uint32_t*>(dst + 2 * lane + 64 * e) = pack_half(o[e].x * inv, o[e].y * inv, p.bf16);
 }
 
-template <int D, int GS, bool SPLIT>
+template <int D, int GS, bool SPLIT, bool MASK>
 cudaError_t launch_it(Prompt& p, cudaStream_t s) {
   static bool done[64] = {};
   constexpr int bytes = PLayout<D, GS>::BYTES;
-  cudaError_t e = allow_smem(prompt_kernel<D, GS, SPLIT>, bytes, done);
+  cudaError_t e = allow_smem(prompt_kernel<D, GS, SPLIT, MASK>, bytes, done);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.tiles * p.a.c.heads * p.a.batch, total = items * p.parts;
   if (total >= (1ll << 30) || !encode_rows(&p.tk, p.a.c.k, p.a.c, D, 1 << p.a.c.page_shift) ||
       !encode_rows(&p.tv, p.a.c.v, p.a.c, D, 1 << p.a.c.page_shift))
     return cudaErrorInvalidValue;
-  e = launch(prompt_kernel<D, GS, SPLIT>, dim3((unsigned)total), THREADS, bytes, s, p);
+  e = launch(prompt_kernel<D, GS, SPLIT, MASK>, dim3((unsigned)total), THREADS, bytes, s, p);
   if (e != cudaSuccess || !SPLIT) return e;
   return launch(join_rows_kernel<D>, dim3((unsigned)(items * (CTA_ROWS / JOIN_WARPS))),
                 32 * JOIN_WARPS, 0, s, p);
@@ -802,15 +827,16 @@ cudaError_t launch_it(Prompt& p, cudaStream_t s) {
 
 template <int D, int GS>
 cudaError_t launch_parts(Prompt& p, cudaStream_t s) {
-  return p.parts > 1 ? launch_it<D, GS, true>(p, s) : launch_it<D, GS, false>(p, s);
+  if (p.mask) return p.parts > 1 ? launch_it<D, GS, true, true>(p, s) : launch_it<D, GS, false, true>(p, s);
+  return p.parts > 1 ? launch_it<D, GS, true, false>(p, s) : launch_it<D, GS, false, false>(p, s);
 }
 
 // Parts of an item: enough to give every SM one, of two steps at least. Measured
 // on one sequence, 8 kv heads and groups of 4, split against not: 128 queries over
 // 32768 tokens 76 against 425 us, 64 over 2048 26 against 37 us, 256 over 1024 29
 // against 25 us: sums in fp32 and a second launch cost about 14 us, eight steps.
-int prompt_parts(long long items, int max_kv) {
-  const long long steps = ((long long)max_kv + KT - 1) / KT;
+int prompt_parts(long long items, long long max_kv) {
+  const long long steps = (max_kv + KT - 1) / KT;
   if (steps < SPLIT_STEPS) return 1;
   return (int)std::max<long long>(1, std::min<long long>({SPLIT_SMS / items, steps / 2, 32}));
 }
@@ -823,12 +849,14 @@ size_t prompt_workspace_bytes(int batch, int max_q, int max_kv, int group, int k
   return parts > 1 ? (size_t)(items * parts) * CTA_ROWS * (dim + 2) * 4 : 0;
 }
 
-cudaError_t launch_prompt(const Attn& a, int dim, int bf16, void* workspace, cudaStream_t s) {
+cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* workspace, cudaStream_t s) {
   Prompt p;
   p.a = a;
   p.bf16 = bf16;
+  p.mask = mask;
   p.tiles = (int)(((long long)a.max_q * a.group + CTA_ROWS - 1) / CTA_ROWS);
-  p.parts = prompt_parts((long long)p.tiles * a.c.heads * a.batch, a.max_kv);
+  // (no more parts than the workspace has room for, which counts all tokens)
+  p.parts = prompt_parts((long long)p.tiles * a.c.heads * a.batch, seen_at_most(a, CTA_ROWS / a.group + 2));
   p.sums = static_cast<float*>(workspace);
   if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, s) : launch_parts<64, 16>(p, s);
   return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, s) : launch_parts<128, 16>(p, s);
