@@ -577,6 +577,25 @@ W4_API w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w
                                          void* stream);
 
 /*
+ * After a tree of drafts was checked: of sequence b's n = cu_q[b+1] - cu_q[b] drafts,
+ * its last n tokens (kv_lens counts them), those listed in path[cu_q[b] .. cu_q[b+1])
+ * stay, the first as its token kv_lens[b] - n and so on, whatever page they were in.
+ *   path     [total_q] int32: draft numbers 0..n-1, ascending, then -1 (any negative
+ *            number) up to the sequence's end; all -1: none stays.
+ * A page that gets tokens takes the largest of the scales of the pages they come from
+ * and, if tokens of the sequence stay in it, its own; codes are stored again as
+ * e4m3(code * (s / s')), in fp32, where that changes the scale. Codes of tokens that do
+ * not stay are left as they are. kv_lens is read only: shorten the sequences by
+ * w4_kv8_shorten after the call for the last layer's cache. The pages concerned belong
+ * to one sequence. max_q_len: 64 at most (W4_ERR_SHAPE); table, kv_lens and cu_q as for
+ * w4_kv8_append. A sequence that those bounds leave out, with a bad page number among
+ * those of its drafts, or whose path is none, is left as it is (W4_ERR_PAGE).
+ */
+W4_API w4_status w4_kv8_keep(const w4_kv8_cache* cache, const int32_t* table, int table_stride,
+                             const int32_t* kv_lens, const int32_t* cu_q, const int32_t* path,
+                             int batch, int total_q, int max_q_len, void* stream);
+
+/*
  * The pages of a pool are counted by refs [num_pages] int32 (0: free), and its
  * sequences described by table [num_seqs][table_stride] and lens [num_seqs]
  * (tokens held; 0: an empty slot). Table entries past a sequence's pages are -1: lens
@@ -587,12 +606,17 @@ W4_API w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w
  * stream order; with status_out NULL an error goes to the device status word.
  * Results depend on the inputs alone: pages are handed out in ascending order.
  * `workspace`: w4_kv8_pages_workspace_size(num_pages, n) bytes, n the number of
- * sequences or pairs given (num_seqs for reserve and compact).
+ * sequences or pairs given (num_seqs for reserve and compact; shorten needs none).
  *
  * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0; at most 2^30 tokens then)
  *     for every sequence, and gives it the pages that takes: the lowest free ones,
  *     sequence by sequence. (After an error lens is what it was, and an append that
  *     still follows, in a graph say, takes the last tokens counted there for its own.)
+ * w4_kv8_shorten  lens[s] -= drop[s] (0 to lens[s]) for every sequence: the pages
+ *     beyond its new end lose a reference and leave its table row. A drop or length
+ *     out of range, or a bad or free page among those, changes nothing (W4_ERR_PAGE).
+ *     (Tables that name a page more often than its references say are found only while
+ *     they are changed: such a page stays free, and the call reports W4_ERR_PAGE.)
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
  *     of src[i], which may be an earlier pair's target. Full pages are shared
  *     (refs + 1); a last partial page is copied into the next free page, which
@@ -617,6 +641,9 @@ W4_API w4_status w4_kv8_reserve(int32_t* refs, int num_pages, int32_t* table, in
                                 int32_t* lens, int num_seqs, const int32_t* new_tokens,
                                 int page_size, int32_t* status_out, void* workspace,
                                 size_t workspace_bytes, void* stream);
+W4_API w4_status w4_kv8_shorten(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                                int32_t* lens, int num_seqs, const int32_t* drop, int page_size,
+                                int32_t* status_out, void* stream);
 W4_API w4_status w4_kv8_fork(int32_t* refs, int num_pages, int32_t* table, int table_stride,
                              int32_t* lens, int num_seqs, const int32_t* src, const int32_t* dst,
                              int n, int page_size, int32_t* copy_src, int32_t* copy_dst,

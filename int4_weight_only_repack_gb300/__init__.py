@@ -25,6 +25,7 @@ __all__ = [
     "RepackedLayer", "repack_awq", "repack_gptq", "linear", "w4a16_moe_gemm", "RepackedExperts",
     "repack_awq_experts", "moe_linear",
     "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "w4_kv8_attention_workspace_size",
+    "kv8_keep", "kv8_shorten",
     "KV8Pool", "kv8_pool", "kv8_reserve", "kv8_fork", "kv8_free", "kv8_compact", "kv8_copy_pages",
     "w4_kv8_pages_workspace_size", "qk_norm_rope", "rope_table",
 ]
@@ -118,6 +119,10 @@ _SIGNATURES = {
     "w4_kv8_pages_workspace_size": (_c_size, [_c_int, _c_int]),
     "w4_kv8_reserve": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int,
                                 _c_void_p, _c_int, _c_void_p, _c_void_p, _c_size, _c_void_p]),
+    "w4_kv8_keep": (_c_int, [_c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_int,
+                             _c_int, _c_int, _c_void_p]),
+    "w4_kv8_shorten": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
+                                _c_int, _c_void_p, _c_void_p]),
     "w4_kv8_fork": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p,
                              _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
                              _c_void_p, _c_size, _c_void_p]),
@@ -802,6 +807,21 @@ def kv8_attention(q, cache: KV8Cache, table, kv_lens, cu_q, max_q_len, max_kv_le
     return out
 
 
+def kv8_keep(cache: KV8Cache, table, kv_lens, cu_q, path, max_q_len, stream=None):
+    """Keeps the accepted ones of each sequence's drafts, which are its last tokens
+    (kv_lens counts them): path int32 [tokens], packed like the drafts, lists their
+    numbers within the sequence, ascending, then -1. They become the sequence's first
+    new tokens, in every layer's cache that this is called for; then shorten the
+    sequences with kv8_shorten. See w4_kv8_keep in include/w4a16.h."""
+    _one_gpu(cache._device, table, kv_lens, cu_q, path)
+    tab, stride, held = _table(table, stream, cache._device)
+    status = lib().w4_kv8_keep(cache._ref, tab, stride, _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"),
+                               _ints(path, "path"), _batch(table, kv_lens, cu_q), path.shape[0],
+                               max_q_len, _on(stream, cache._device))
+    if status:
+        _check(status)
+
+
 class KV8Pool(_Handle):
     """The pages of a pool and the sequences that hold them: refs [pages] (0: a
     free page), table [sequences, pages of the longest] (-1 past a sequence's
@@ -853,6 +873,18 @@ def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
     status = lib().w4_kv8_reserve(*pool._args, _ints(new_tokens, "new_tokens"), pool.page_size,
                                   pool._status,
                                   *_space(pool._bytes, pool._device, handle, stream), handle)
+    if status:
+        _check(status)
+
+
+def kv8_shorten(pool: KV8Pool, drop, stream=None):
+    """Takes the last drop[s] tokens from every sequence s (rejected drafts, say): the pages
+    beyond its new end lose a reference."""
+    if drop.shape[0] != pool._args[5]:
+        raise ValueError("drop must have an entry for every sequence")
+    _one_gpu(pool._device, drop)
+    status = lib().w4_kv8_shorten(*pool._args, _ints(drop, "drop"), pool.page_size, pool._status,
+                                  _on(stream, pool._device))
     if status:
         _check(status)
 

@@ -324,6 +324,26 @@ w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w4_kv8_c
                 max_kv_len, heads, *mask, dtype, workspace, workspace_bytes, stream);
 }
 
+w4_status w4_kv8_keep(const w4_kv8_cache* cache, const int32_t* table, int table_stride,
+                      const int32_t* kv_lens, const int32_t* cu_q, const int32_t* path, int batch,
+                      int total_q, int max_q_len, void* stream) {
+  w4_status st = check_cache(cache);
+  if (st) return st;
+  if ((st = check_batch(table, table_stride, kv_lens, cu_q, batch, total_q, max_q_len, W4_F16))) return st;
+  if (max_q_len > MAX_DRAFTS) return W4_ERR_SHAPE;
+  if (batch == 0 || total_q == 0 || max_q_len == 0) return W4_OK;
+  if (!path) return W4_ERR_NULL;
+  if (!aligned4(path)) return W4_ERR_ALIGN;
+  if (overlaps_cache(cache, table, table_bytes(batch, table_stride)) ||
+      overlaps_cache(cache, kv_lens, (size_t)batch * 4) || overlaps_cache(cache, cu_q, (size_t)(batch + 1) * 4) ||
+      overlaps_cache(cache, path, (size_t)total_q * 4) || cache_overlaps_itself(cache))
+    return W4_ERR_ALIAS;
+  if ((st = check_arch())) return st;
+  const KeepArgs a{device_cache(cache), table, kv_lens, cu_q, path, table_stride, batch, total_q, max_q_len,
+                   cache->head_dim};
+  return from_cuda(launch_keep(a, static_cast<cudaStream_t>(stream)));
+}
+
 size_t w4_kv8_pages_workspace_size(int num_pages, int n) {
   if (num_pages < 1 || num_pages > MAX_PAGES || n < 0 || n > MAX_BATCH) return 0;
   return pages_workspace_bytes(num_pages, n);
@@ -350,6 +370,24 @@ w4_status w4_kv8_reserve(int32_t* refs, int num_pages, int32_t* table, int table
   BookArgs a{refs, table, lens, num_pages, table_stride, num_seqs, shift_of(page_size), new_tokens,
              nullptr, num_seqs, nullptr, nullptr, status_out, workspace};
   return from_cuda(launch_reserve(a, static_cast<cudaStream_t>(stream)));
+}
+
+w4_status w4_kv8_shorten(int32_t* refs, int num_pages, int32_t* table, int table_stride,
+                         int32_t* lens, int num_seqs, const int32_t* drop, int page_size,
+                         int32_t* status_out, void* stream) {
+  w4_status st = check_pool(refs, num_pages, table, table_stride, num_seqs);
+  if (st) return st;
+  if ((st = check_page_size(page_size))) return st;
+  if (num_seqs > 0 && (!lens || !drop)) return W4_ERR_NULL;
+  if (!aligned4(lens) || !aligned4(drop) || !aligned4(status_out)) return W4_ERR_ALIGN;
+  const size_t s4 = (size_t)num_seqs * 4;
+  const Extent e[5] = {{refs, (size_t)num_pages * 4}, {table, table_bytes(num_seqs, table_stride)}, {lens, s4},
+                       {status_out, status_out ? 4u : 0u}, {drop, s4}};
+  if (any_alias(e, 5, 4)) return W4_ERR_ALIAS;
+  if ((st = check_arch())) return st;
+  BookArgs a{refs, table, lens, num_pages, table_stride, num_seqs, shift_of(page_size), drop, nullptr,
+             num_seqs, nullptr, nullptr, status_out, nullptr};
+  return from_cuda(launch_shorten(a, static_cast<cudaStream_t>(stream)));
 }
 
 w4_status w4_kv8_fork(int32_t* refs, int num_pages, int32_t* table, int table_stride,

@@ -47,6 +47,13 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 
+struct KeepArgs {
+  Cache c;
+  const int32_t *table, *kv_lens, *cu_q, *path;
+  int table_stride, batch, total_q, max_q, dim;
+};
+cudaError_t launch_keep(const KeepArgs& a, cudaStream_t s);
+
 struct AttnArgs {
   const uint16_t* q;
   size_t q_stride;
@@ -66,7 +73,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s);
 struct BookArgs {
   int32_t *refs, *table, *lens;
   int pages, table_stride, seqs, page_shift;
-  const int32_t *list, *list2;  // new_tokens; or src, dst; or seqs
+  const int32_t *list, *list2;  // new_tokens; or drop; or src, dst; or seqs
   int n;
   int32_t *copy_src, *copy_dst;
   int32_t* status_out;
@@ -75,6 +82,7 @@ struct BookArgs {
 size_t pages_workspace_bytes(int num_pages, int n);
 cudaError_t launch_reserve(const BookArgs& a, cudaStream_t s);
 cudaError_t launch_fork(const BookArgs& a, cudaStream_t s);
+cudaError_t launch_shorten(const BookArgs& a, cudaStream_t s);
 cudaError_t launch_free(const BookArgs& a, cudaStream_t s);
 cudaError_t launch_compact(const BookArgs& a, cudaStream_t s);
 cudaError_t launch_copy_pages(const Cache& c, int dim, const int32_t* src, const int32_t* dst,

@@ -1,4 +1,4 @@
-// Pages of the 8-bit key-value cache: reserve, fork, free, compact, copy.
+// Pages of the 8-bit key-value cache: reserve, shorten, fork, free, compact, copy.
 //
 // The reference counts are the only record of which pages are free. "The
 // lowest free pages, in order" is a stream compaction of refs == 0, so the
@@ -343,6 +343,69 @@ __global__ void __launch_bounds__(128) free_kernel(const Book b) {
   }
 }
 
+// Sequences get shorter. One CTA, a thread a sequence at a time: first all is looked at,
+// then, if nothing is wrong, all is done. The pages that a warp's 32 sequences give back
+// are dealt to its lanes, however many each has.
+__global__ void __launch_bounds__(BT) shorten_kernel(const Book b) {
+  grid_wait();
+  grid_launch_dependents();
+  int* status = b.status_out ? b.status_out : b.status;
+  const int lane = lane_id();
+  int err = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    bool refused = false;  // a page with fewer references than tables that name it
+    for (int s0 = 0; s0 < b.seqs; s0 += BT) {
+      const int s = s0 + threadIdx.x;
+      const int drop = s < b.seqs ? b.list[s] : 0, toks = s < b.seqs ? b.lens[s] : 0;
+      int first = 0, pages = 0;
+      if (drop != 0) {
+        if (drop < 0 || toks < drop || toks > MAX_KV || toks > ((long long)b.stride << b.shift)) {
+          err = W4_ERR_PAGE;
+        } else {
+          first = pages_of(toks - drop, b.shift);
+          pages = pages_of(toks, b.shift) - first;
+          if (pass) b.lens[s] = toks - drop;
+        }
+      }
+      long long end = pages;  // the warp's pages up to this lane's last
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(~0u, end, d);
+        if (lane >= d) end += u;
+      }
+      const long long all = __shfl_sync(~0u, end, 31);
+      for (long long i0 = 0; i0 < all; i0 += 32) {
+        const long long i = i0 + lane;
+        int who = 0;  // the first lane whose end lies past i
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+          if (__shfl_sync(~0u, end, who + d - 1) <= i) who += d;
+        who = min(who, 31);
+        const long long begin = __shfl_sync(~0u, end - pages, who);
+        const int f = __shfl_sync(~0u, first, who), of = __shfl_sync(~0u, s, who);
+        if (i >= all) continue;
+        int32_t* entry = b.table + (size_t)of * b.stride + f + (i - begin);
+        const int p = *entry;
+        if (!pass) {
+          if (p < 0 || p >= b.pages || b.refs[p] <= 0) err = W4_ERR_PAGE;
+        } else {
+          *entry = -1;
+          if (atomicSub(&b.refs[p], 1) <= 0) {  // it has become free: leave it so
+            atomicAdd(&b.refs[p], 1);
+            refused = true;
+          }
+        }
+      }
+    }
+    err = __syncthreads_or(pass ? refused : err) ? W4_ERR_PAGE : 0;
+    if (err) break;
+  }
+  if (threadIdx.x == 0) {
+    if (b.status_out) *status = err;
+    else if (err) record(status, err);
+  }
+}
+
 __global__ void clear_status_kernel(int32_t* status) {
   grid_wait();
   grid_launch_dependents();
@@ -551,6 +614,13 @@ cudaError_t launch_free(const BookArgs& a, cudaStream_t s) {
     return e;
   if (a.n == 0) return cudaSuccess;
   return launch(free_kernel, dim3(a.n), 128, 0, s, book(a, status));
+}
+
+cudaError_t launch_shorten(const BookArgs& a, cudaStream_t s) {
+  int* status = nullptr;
+  const cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return e;
+  return launch(shorten_kernel, dim3(1), BT, 0, s, book(a, status));
 }
 
 cudaError_t launch_compact(const BookArgs& a, cudaStream_t s) {
