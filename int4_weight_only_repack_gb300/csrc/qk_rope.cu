@@ -11,6 +11,11 @@
 // rotated, 2 l and 2 l + 1. Either way its cosines are 8 l to 8 l + 7 of a table row.
 //
 // Everything is fp32 from the loads to the one rounding at the end.
+//
+// Bound by memory: a prompt of 8000 tokens of 32 + 8 heads of 128 (168 MB) takes 30 us,
+// 5.6 TB/s (one of 4000, which fits in L2, 12.9 us); one token
+// 1.7 us in a graph, a launch's latency. A thread that goes on to its next heads while
+// their elements are on their way (registers for two shares) was no faster: 34 to 44 us.
 #include "kv8_device.cuh"
 #include "w4a16_device.cuh"
 
@@ -18,7 +23,7 @@ namespace w4 {
 namespace kv8 {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 64;  // (blocks of 256 end in steps: 31.4 against 30.0 us on a prompt of 8000)
 
 struct Side {
   const uint16_t* in;
@@ -69,32 +74,35 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
   grid_launch_dependents();
   const int l = threadIdx.x % TEAM;
   const int per = r.side[0].teams + r.side[1].teams;
-  const long long team = (long long)blockIdx.x * (THREADS / TEAM) + threadIdx.x / TEAM;
-  const int tok = (int)(team / per);
-  int slot = (int)(team - (long long)tok * per);
+  // the block's first team, and this thread's from there (one long division a block)
+  const long long team0 = (long long)blockIdx.x * (THREADS / TEAM);
+  const int tok0 = (int)(team0 / per);
+  int slot = (int)(team0 - (long long)tok0 * per) + threadIdx.x / TEAM;
+  const int tok = tok0 + slot / per;
+  slot -= (tok - tok0) * per;
   const int which = slot >= r.side[0].teams;
   const Side& s = r.side[which];
   if (which) slot -= r.side[0].teams;
-  // (whole teams drop out, but their lanes stay for the shuffles)
-  bool live = tok < r.tokens;
-  const int pos = live && r.positions ? r.positions[tok] : 0;
-  if (pos < 0) live = false;  // a padded token
-  if (live && r.table && pos >= r.rows) {
-    live = false;
-    if (l == 0) record(r.status, W4_ERR_POSITION);
-  }
+  const bool here = tok < r.tokens;
+  const int pos = here && r.positions ? r.positions[tok] : 0;
   const bool turns = r.table && l < r.rot / 16;
   const int first = !INTERLEAVED && turns ? l : 2 * l, second = !INTERLEAVED && turns ? l + r.rot / 16 : 2 * l + 1;
-  uint4 x[HEADS][2];
+  uint4 x[HEADS][2];  // (of padding too: its position is still on its way; read for the last time)
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int h = slot + i * s.teams;
     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-    if (live && h < s.heads) {
+    if (here && h < s.heads) {
       const uint16_t* from = s.in + (size_t)tok * s.in_stride + (size_t)h * D;
-      x[i][0] = *reinterpret_cast<const uint4*>(from + 8 * first);
-      x[i][1] = *reinterpret_cast<const uint4*>(from + 8 * second);
+      x[i][0] = __ldcs(reinterpret_cast<const uint4*>(from + 8 * first));
+      x[i][1] = __ldcs(reinterpret_cast<const uint4*>(from + 8 * second));
     }
+  }
+  // (whole teams drop out, but their lanes stay for the shuffles)
+  bool live = here && pos >= 0;
+  if (live && r.table && pos >= r.rows) {
+    live = false;
+    if (l == 0) record(r.status, W4_ERR_POSITION);
   }
   float c[8], sn[8], w[2][8];
   if (live && turns) {
@@ -102,7 +110,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
     load8(row, c);
     load8(row + r.rot / 2, sn);
   }
-  if (live && s.weight) {
+  if (here && s.weight) {
     load8(s.weight + 8 * first, w[0]);
     load8(s.weight + 8 * second, w[1]);
   }
@@ -154,18 +162,35 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
   }
 }
 
-template <int D, bool BF16, bool INTERLEAVED>
+template <int D, bool BF16, bool INTERLEAVED, int HEADS>
 cudaError_t launch_heads(Rope& r, cudaStream_t s) {
   constexpr int TEAMS = THREADS / (D / 16);  // of a block
-  for (Side& side : r.side) side.teams = side.heads;
+  for (Side& side : r.side) side.teams = (side.heads + HEADS - 1) / HEADS;
   const long long teams = (long long)r.tokens * (r.side[0].teams + r.side[1].teams);
-  return launch(rope_kernel<D, BF16, INTERLEAVED, 1>, dim3((unsigned)((teams + TEAMS - 1) / TEAMS)), THREADS, 0, s, r);
+  return launch(rope_kernel<D, BF16, INTERLEAVED, HEADS>, dim3((unsigned)((teams + TEAMS - 1) / TEAMS)), THREADS, 0, s, r);
+}
+
+// How many heads a team takes: one while that leaves the GPU half empty, where latency
+// counts; more where the table and the weights, 128 bytes a thread from the L1 cache for
+// 64 of a head's, would be what the kernel waits for. In us, replayed in a graph, 40 heads
+// of 128 (1 / 4 / 8 heads a team): 64 tokens 1.9 / 2.5 / 3.4, 200 2.4 / 2.6 / 3.4, 350
+// 3.3 / 2.9 / 3.6, 1500 8.2 / 6.1 / 6.3, 4000 21.2 / 12.9 / 13.4, 5500 29.7 / 22.7 / 21.2,
+// 8000 42.3 / 33.2 / 30.0; 32 heads of 64: 333 2.1 / 2.6 / 3.3, 1000 3.1 / 3.0 / 4.0, 8000
+// 16.6 / 10.2 / 12.1, 16000 34.1 / 23.9 / 24.4.
+constexpr long long FEW_THREADS = 100000, MANY_THREADS = 1400000;  // with one head a team
+
+template <int D, bool BF16, bool INTERLEAVED>
+cudaError_t launch_pick(Rope& r, cudaStream_t s) {
+  const long long threads = (long long)r.tokens * (r.side[0].heads + r.side[1].heads) * (D / 16);
+  if (threads <= FEW_THREADS) return launch_heads<D, BF16, INTERLEAVED, 1>(r, s);
+  if (threads <= MANY_THREADS) return launch_heads<D, BF16, INTERLEAVED, 4>(r, s);
+  return launch_heads<D, BF16, INTERLEAVED, 8>(r, s);
 }
 
 template <int D>
 cudaError_t launch_d(Rope& r, int bf16, int interleaved, cudaStream_t s) {
-  if (interleaved) return bf16 ? launch_heads<D, true, true>(r, s) : launch_heads<D, false, true>(r, s);
-  return bf16 ? launch_heads<D, true, false>(r, s) : launch_heads<D, false, false>(r, s);
+  if (interleaved) return bf16 ? launch_pick<D, true, true>(r, s) : launch_pick<D, false, true>(r, s);
+  return bf16 ? launch_pick<D, true, false>(r, s) : launch_pick<D, false, false>(r, s);
 }
 
 }  // namespace
