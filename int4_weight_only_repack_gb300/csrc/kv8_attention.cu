@@ -921,6 +921,19 @@ bool many_rows(int max_q, int group) { return (long long)max_q * group > 64; }
 
 bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX_SCAN; }
 
+// Calls whose windows are short enough for items of their own, however long the
+// sequences are: the windows even out what an item has to read, so it pays longer than
+// ITEM_TOKENS allows, while there are few items. Of their own against split, in us, 4 sinks:
+//   sequences of heads   window 256       600        1000         1500         2000
+//     1 of 32 on 8      6.9 / 11.6   9.6 / 12.7  12.4 / 12.5  15.8 / 12.8  19.3 / 12.4
+//    64 of 64 on 8     15.1 / 17.7  22.3 / 24.4  31.3 / 34.5  41.7 / 45.2  51.1 / 55.2
+//   256 of 32 on 8     59.0 / 39.5  81.0 / 66.9   105 / 97.0   142 / 138    177 / 176
+bool windows_are_short(const Attn& a) {
+  const long long seen = seen_at_most(a, a.max_q);
+  const long long items = (long long)a.batch * a.c.heads * (((long long)a.max_q * a.group + 15) / 16);
+  return seen < a.max_kv && seen <= 1024 && items <= 1024;
+}
+
 // Rows of queries that share one widening of the codes, in eights.
 int row_blocks(long long rows) { return rows > 8 ? 2 : 1; }
 
@@ -998,7 +1011,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s) {
   const int box = std::min(1 << a.c.page_shift, STEP);
   if (!encode_rows(&r.tk, a.c.k, a.c, a.dim, box) || !encode_rows(&r.tv, a.c.v, a.c, a.dim, box))
     return cudaErrorInvalidValue;
-  r.split = splits(a.batch, (int)seen_at_most(r.a, r.a.max_q));
+  r.split = splits(a.batch, a.max_kv) && !windows_are_short(r.a);
   r.bf16 = a.bf16;
   r.rec = static_cast<int*>(a.workspace);
   r.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + MAX_WORKERS * sizeof(Begun));

@@ -75,7 +75,7 @@ struct Prompt {
   int tiles;           // of the longest sequence, of CTA_ROWS rows
   int parts;           // of an item
   int bf16, mask;
-  float* sums;         // with parts > 1: [item][part][CTA_ROWS][D + 2], sums, maximum, l
+  float* sums;         // with parts > 1: [item][part][D + 2][CTA_ROWS], sums, maximum, l
 };
 
 // GS: tokens that share a scale, 16 or 64 (the page's, where it has that many).
@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       constexpr bool whole = !SPLIT;
       const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
       uint16_t* dst = a.out + ((size_t)(s.q0 + tok) * a.q_heads + h * a.group + (row - tok * a.group)) * D;
-      float* sum = whole ? nullptr : p.sums + ((size_t)blockIdx.x * CTA_ROWS + TILE_ROWS * i + lrow) * (D + 2);
+      // (a column of sums at a time: a warp's rows are neighbours there)
+      float* sum = whole ? nullptr : p.sums + (size_t)blockIdx.x * CTA_ROWS * (D + 2) + TILE_ROWS * i + lrow;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t y[32];
@@ -528,12 +529,14 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                            pack_half(f[4], f[5], p.bf16), pack_half(f[6], f[7], p.bf16));
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
-              *reinterpret_cast<float2*>(sum + 32 * c + k + e) = make_float2(f[e], f[e + 1]);
+            for (int e = 0; e < 8; ++e) sum[(32 * c + k + e) * CTA_ROWS] = f[e];
           }
         }
       }
-      if (!whole && real) *reinterpret_cast<float2*>(sum + D) = make_float2(room == NEG_INF ? NEG_INF : m, l);
+      if (!whole && real) {
+        sum[D * CTA_ROWS] = room == NEG_INF ? NEG_INF : m;
+        sum[(D + 1) * CTA_ROWS] = l;
+      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ pages to operand tiles
@@ -758,55 +761,72 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   }
 }
 
-// One row of an item that several CTAs shared, a warp: lanes take columns, and
-// first the parts' maxima.
-constexpr int JOIN_WARPS = 8;
+// Joins the parts of 32 rows and 32 columns of an item that several CTAs shared: first a
+// warp takes a row, its lanes the parts' maxima and sums of weights; then a lane has a row
+// and a warp four columns, so that reads of the sums are whole lines.
+constexpr int JOIN_ROWS = 32, JOIN_COLS = 32, JOIN_WARPS = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid_constant__ Prompt p) {
-  constexpr int V = D / 64;
+  __shared__ float f_sh[JOIN_ROWS][33], l_sh[JOIN_ROWS];  // a part's factor (-1: it saw nothing), and 1 / l
+  __shared__ float o_sh[JOIN_ROWS][JOIN_COLS + 1];
   grid_wait();
   grid_launch_dependents();
   const Attn& a = p.a;
-  const int lane = threadIdx.x & 31, lrow = (blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5)) % CTA_ROWS;
-  const int item = blockIdx.x / (CTA_ROWS / JOIN_WARPS);
+  constexpr int COLS = D / JOIN_COLS, ROWS = CTA_ROWS / JOIN_ROWS;  // blocks of an item
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col0 = blockIdx.x % COLS * JOIN_COLS, lrow0 = blockIdx.x / COLS % ROWS * JOIN_ROWS;
+  const int item = blockIdx.x / (COLS * ROWS);
   const int items = a.batch * a.c.heads, tile = p.tiles - 1 - item / items, bh = item % items;
   const int b = bh / a.c.heads, h = bh - b * a.c.heads;
   const Seq s = load_seq(a, b);
-  const int row = tile * CTA_ROWS + lrow;
-  if (row >= s.n * a.group || s.n > a.max_q) return;
-  const size_t pitch = (size_t)CTA_ROWS * (D + 2);
-  const float* from = p.sums + (size_t)item * p.parts * pitch + lrow * (D + 2);
-  float2 ml = make_float2(NEG_INF, 0.f);  // (at most 32 parts)
-  if (lane < p.parts) ml = *reinterpret_cast<const float2*>(from + lane * pitch + D);
-  float top = ml.x;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  const float base = top == NEG_INF ? 0.f : top;
-  const bool none = ml.x == NEG_INF && ml.y == 0.f;  // (a part that saw only NaN has an l that is not 0)
-  const float f = none ? 0.f : ex2(ml.x - base);
-  float l = none ? 0.f : ml.y * f;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  float2 o[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < p.parts; ++k) {
-    const float fk = __shfl_sync(~0u, f, k);
-    const bool skip = __shfl_sync(~0u, none, k);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float2 y = *reinterpret_cast<const float2*>(from + k * pitch + 2 * lane + 64 * e);
-      o[e].x += skip ? 0.f : y.x * fk;
-      o[e].y += skip ? 0.f : y.y * fk;
+  const int row0 = tile * CTA_ROWS + lrow0, rows = min(s.n * a.group - row0, JOIN_ROWS);
+  if (rows <= 0 || s.n > a.max_q) return;
+  constexpr size_t PITCH = (size_t)CTA_ROWS * (D + 2);
+  const float* from = p.sums + (size_t)item * p.parts * PITCH + lrow0;
+  for (int r = warp; r < rows; r += JOIN_WARPS) {
+    float2 ml = make_float2(NEG_INF, 0.f);  // (at most 32 parts)
+    if (lane < p.parts) {
+      const float* at = from + lane * PITCH + D * CTA_ROWS + r;
+      ml = make_float2(at[0], at[CTA_ROWS]);
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int tok = row / a.group;
-  uint16_t* dst = a.out + ((size_t)(s.q0 + tok) * a.q_heads + h * a.group + (row - tok * a.group)) * D;
+    float top = ml.x;
 #pragma unroll
-  for (int e = 0; e < V; ++e)
-    *reinterpret_cast<uint32_t*>(dst + 2 * lane + 64 * e) = pack_half(o[e].x * inv, o[e].y * inv, p.bf16);
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float base = top == NEG_INF ? 0.f : top;
+    const bool none = ml.x == NEG_INF && ml.y == 0.f;  // (a part that saw only NaN has an l that is not 0)
+    const float f = none ? 0.f : ex2(ml.x - base);
+    float l = none ? 0.f : ml.y * f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    f_sh[r][lane] = none ? -1.f : f;
+    if (lane == 0) l_sh[r] = l == 0.f ? 0.f : 1.f / l;
+  }
+  __syncthreads();
+  constexpr int V = JOIN_COLS / JOIN_WARPS;
+  if (lane < rows) {
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < p.parts; ++k) {
+      const float f = f_sh[lane][k];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float y = from[k * PITCH + (size_t)(col0 + V * warp + e) * CTA_ROWS + lane];
+        o[e] += f < 0.f ? 0.f : y * f;
+      }
+    }
+    const float inv = l_sh[lane];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o_sh[lane][V * warp + e] = o[e] * inv;
+  }
+  __syncthreads();
+  const int r = threadIdx.x / JOIN_WARPS, c = threadIdx.x % JOIN_WARPS * V, row = row0 + r;
+  if (r >= rows) return;
+  const int tok = row / a.group;
+  uint16_t* dst = a.out + ((size_t)(s.q0 + tok) * a.q_heads + h * a.group + (row - tok * a.group)) * D + col0 + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half(o_sh[r][c], o_sh[r][c + 1], p.bf16),
+                                              pack_half(o_sh[r][c + 2], o_sh[r][c + 3], p.bf16));
 }
 
 template <int D, int GS, bool SPLIT, bool MASK>
@@ -821,7 +841,7 @@ cudaError_t launch_it(Prompt& p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   e = launch(prompt_kernel<D, GS, SPLIT, MASK>, dim3((unsigned)total), THREADS, bytes, s, p);
   if (e != cudaSuccess || !SPLIT) return e;
-  return launch(join_rows_kernel<D>, dim3((unsigned)(items * (CTA_ROWS / JOIN_WARPS))),
+  return launch(join_rows_kernel<D>, dim3((unsigned)(items * (CTA_ROWS / JOIN_ROWS) * (D / JOIN_COLS))),
                 32 * JOIN_WARPS, 0, s, p);
 }
 
