@@ -413,16 +413,27 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t bad = nan[c];
-          uint32_t seen = 0;  // tokens of the 32
           if constexpr (MASK) {
-            const int t = t0 + 32 * c, d = t - s.kv + s.n;  // d: the draft that it begins with
-            seen = below32(sees.lim - t) & (~below32(sees.lo - t) | below32(a.sinks - t));
+            // (a step's mask costs what its exponentials do, so a warp applies what it needs of it)
+            const int t = t0 + 32 * c, d = t - s.kv + s.n;  // d: the draft that the 32 tokens begin with
+            uint32_t seen = below32(sees.lim - t) & (~below32(sees.lo - t) | below32(a.sinks - t));
             if (d > -32 && d < MAX_DRAFTS) seen |= (uint32_t)(d < 0 ? sees.bits << -d : sees.bits >> d);
-          }
+            if (bad) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (bad >> k & 1) x[c][k] = 0x7FFFFFFFu;
-            if (MASK ? !(seen >> k & 1) : 32 * c + k >= left) x[c][k] = __float_as_uint(NEG_INF);
+              for (int k = 0; k < 32; ++k)
+                if (bad >> k & 1) x[c][k] = 0x7FFFFFFFu;
+            }
+            if (!__all_sync(~0u, seen == ~0u)) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(seen >> k & 1)) x[c][k] = __float_as_uint(NEG_INF);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (bad >> k & 1) x[c][k] = 0x7FFFFFFFu;
+              if (32 * c + k >= left) x[c][k] = __float_as_uint(NEG_INF);
+            }
           }
         }
       }
@@ -698,11 +709,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             const uint32_t pt = tm + 128 * i, ot = tm + 256 + D * i, v0 = vd + stage * TILE;
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k) umma_ts(ot, pt + 8 * k, v0 + k * 128, IDESC_O, j != 0 || k != 0);
+            umma_commit(bars.odone(i));  // (first: who sees the scores has no older product to take for this one)
             if (j + 1 < n) {
               scores(i, j + 1);
               umma_commit(bars.sfull(i));
             }
-            umma_commit(bars.odone(i));
             // a stage is free once the last tile that uses it has read it
             if (i == 1 || j >= steps1) umma_commit(bars.vfree(stage));
             if (j + 1 < n && (i == 1 || j + 1 >= steps1)) umma_commit(bars.kfree((j + 1) % KV_STAGES));
