@@ -617,6 +617,8 @@ W4_API w4_status w4_kv8_keep(const w4_kv8_cache* cache, const int32_t* table, in
  *     out of range, or a bad or free page among those, changes nothing (W4_ERR_PAGE).
  *     (Tables that name a page more often than its references say are found only while
  *     they are changed: such a page stays free, and the call reports W4_ERR_PAGE.)
+ *     A last page that other sequences share stays shared: a sequence shortened into it
+ *     gets tokens again only after w4_kv8_fork, which copies a last partial page.
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
  *     of src[i], which may be an earlier pair's target. Full pages are shared
  *     (refs + 1); a last partial page is copied into the next free page, which

@@ -343,3 +343,28 @@ def test_a_tree_is_its_branches(w4, heads, kv_heads, dim, dtype, page, window, g
             assert torch.equal(cache.k_scale[p], plain.k_scale[o]) and torch.equal(cache.v_scale[p], plain.v_scale[o])
     held = sum(-(-n // page) for n in pool.lens.tolist())
     assert int((pool.refs > 0).sum()) == held and bool((pool.refs <= 1).all())
+
+
+def test_a_fork_after_shortening_into_a_shared_page(w4):
+    """The page is still the other's: the fork copies it, and new tokens go to the copy."""
+    page, dim = 16, 64
+    pool, cache = w4.kv8_pool(20, 3, 64, page), w4.kv8_cache(20, 1, page, dim)
+    w4.kv8_reserve(pool, ref.ints([40, 0, 0]))
+    x = queries(40, 1, dim, "bf16", 9)
+    w4.kv8_append(x, x, cache, pool.table, pool.lens, ref.bounds([40, 0, 0]), 40)
+    w4.kv8_copy_pages(cache, *w4.kv8_fork(pool, ref.ints([0]), ref.ints([1])))
+    w4.kv8_shorten(pool, ref.ints([0, 20, 0]))  # 20 tokens: the second page is the parent's too
+    before = [y[pool.table[0, :3].long()].clone() for y in cache_state_tensors(cache)]
+    moves = w4.kv8_fork(pool, ref.ints([1]), ref.ints([2]))
+    w4.kv8_copy_pages(cache, *moves)
+    assert moves[0].tolist() == [int(pool.table[0, 1])] and int(pool.table[2, 1]) == int(moves[1])
+    w4.kv8_reserve(pool, ref.ints([0, 0, 5]))
+    y = queries(5, 1, dim, "bf16", 10)
+    w4.kv8_append(y, y, cache, pool.table, pool.lens, ref.bounds([0, 0, 5]), 5)
+    assert int(pool.status) == 0
+    for now, was in zip(cache_state_tensors(cache), before):
+        assert torch.equal(now[pool.table[0, :3].long()], was)
+
+
+def cache_state_tensors(cache):
+    return [cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale]
