@@ -887,7 +887,12 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
   p.mask = mask;
   p.tiles = (int)(((long long)a.max_q * a.group + CTA_ROWS - 1) / CTA_ROWS);
   // (no more parts than the workspace has room for, which counts all tokens)
-  p.parts = prompt_parts((long long)p.tiles * a.c.heads * a.batch, seen_at_most(a, CTA_ROWS / a.group + 2));
+  const long long seen = seen_at_most(a, CTA_ROWS / a.group + 2);
+  p.parts = prompt_parts((long long)p.tiles * a.c.heads * a.batch, seen);
+  if (mask && p.parts > 1) {  // none without a step of the longest: 47 steps are 16 parts of 3, not 19
+    const long long steps = (seen + KT - 1) / KT, per = (steps + p.parts - 1) / p.parts;
+    p.parts = (int)((steps + per - 1) / per);
+  }
   p.sums = static_cast<float*>(workspace);
   if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, s) : launch_parts<64, 16>(p, s);
   return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, s) : launch_parts<128, 16>(p, s);
