@@ -563,13 +563,12 @@ def _new(make, stream, index):
     return x
 
 
-def _rows(x, name, heads, dim, shape=None):
+def _rows(x, name, heads, dim):
     """The token stride of x [tokens, heads, dim], whose rows may be slices of a
     wider buffer but whose heads and elements are adjacent."""
-    if shape is None:
-        shape = x.shape
-        if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-            raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {tuple(shape)}")
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], not {tuple(shape)}")
     st = x.stride()
     if shape[0] and (st[2] != 1 or (st[1] != dim and heads > 1)):
         raise ValueError(f"{name}: heads and elements of a token must be adjacent in memory")
@@ -636,23 +635,29 @@ def rope_table(rows, rot_dim, base=10000.0, device="cuda"):
 def _side(x, shape, name, weight, out, stream, index):
     """(w4_head_rows of x [tokens, heads, dim], its output), the output made if None."""
     tokens, heads, dim = shape
-    stride = _rows(x, name, heads, dim, shape)
+    width = heads * dim
+    st = x.stride()
+    if tokens and (st[2] != 1 or (st[1] != dim and heads > 1)):
+        raise ValueError(f"{name}: heads and elements of a token must be adjacent in memory")
     if out is None:
-        out_stride = heads * dim
+        to = width
         if stream is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            out = torch.empty_like(x, memory_format=_CONTIGUOUS)
         else:
-            out = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, index)
+            out = _new(lambda: torch.empty_like(x, memory_format=_CONTIGUOUS), stream, index)
     else:
         if out.shape != shape or out.dtype is not x.dtype:
             raise ValueError(f"{name}_out must have {name}'s shape and type")
-        out_stride = _rows(out, name, heads, dim, shape)
+        to = _rows(out, name + "_out", heads, dim)
     at = None
     if weight is not None:
-        if weight.dtype is not _F32 or weight.dim() != 1 or weight.numel() != dim or not weight.is_contiguous():
+        if weight.dtype is not _F32 or weight.shape != (dim,) or not weight.is_contiguous():
             raise ValueError(f"{name}_weight must be contiguous float32 [{dim}]")
         at = weight.data_ptr()
-    return _HeadRowsStruct(x.data_ptr(), out.data_ptr(), stride, out_stride, at, heads), out
+    return _HeadRowsStruct(x.data_ptr(), out.data_ptr(), st[0] if tokens > 1 else width, to, at, heads), out
+
+
+_CONTIGUOUS = torch.contiguous_format
 
 
 def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -665,39 +670,40 @@ def qk_norm_rope(q, k, positions, table, q_weight=None, k_weight=None, eps=1e-6,
     rotation, then positions may be None. q_weight, k_weight: float32 [dim] of the norms;
     None: no norm. See w4_qk_norm_rope in include/w4a16.h."""
     x = k if q is None else q
-    if x is None or len(x.shape) != 3:
-        raise ValueError("q or k [tokens, heads, dim] is needed")
+    if x is None:
+        raise ValueError("q or k is needed")
     shape, dtype = x.shape, x.dtype
-    tokens, _, dim = shape
+    if len(shape) != 3:
+        raise ValueError("q and k must be [tokens, heads, dim]")
     code = _HALF_CODES.get(dtype)
     if code is None:
         code = dtype_code(dtype)
+    tokens, _, dim = shape
     index = x.get_device()
     _one_gpu(index, *[t for t in (q, k, positions, table, q_weight, k_weight, q_out, k_out) if t is not None])
-    at = rot = None
-    rows = 0
+    at = where = None
+    rows = rot = 0
     if table is not None:
-        if table.dim() != 2 or not table.numel() or table.dtype is not _F32 or not table.is_contiguous():
+        if table.dtype is not _F32 or not table.is_contiguous() or table.dim() != 2 or not table.numel():
             raise ValueError("the table must be contiguous float32 [positions, rot_dim]")
         at, (rows, rot) = table.data_ptr(), table.shape
-    where = None
     if positions is not None:
-        if positions.dim() != 1 or positions.shape[0] != tokens:
+        if positions.shape != (tokens,):
             raise ValueError("positions must have an entry for every token")
         where = _ints(positions, "positions")
     left = right = None
     if q is not None:
-        left, q_out = _side(q, shape, "q", q_weight, q_out, stream, index)
+        side, q_out = _side(q, shape, "q", q_weight, q_out, stream, index)
+        left = ctypes.addressof(side)
     if k is not None:
         if q is not None:
             shape = k.shape
             if len(shape) != 3 or k.dtype is not dtype or shape[0] != tokens or shape[2] != dim:
                 raise ValueError("q and k must have the same type, tokens and head size")
-        right, k_out = _side(k, shape, "k", k_weight, k_out, stream, index)
-    how = _NormRopeStruct(at, rows, rot or 0, interleaved, eps)
-    status = lib().w4_qk_norm_rope(
-        None if left is None else ctypes.addressof(left), None if right is None else ctypes.addressof(right),
-        ctypes.addressof(how), where, tokens, dim, code, _on(stream, index))
+        other, k_out = _side(k, shape, "k", k_weight, k_out, stream, index)
+        right = ctypes.addressof(other)
+    how = _NormRopeStruct(at, rows, rot, interleaved, eps)
+    status = lib().w4_qk_norm_rope(left, right, ctypes.addressof(how), where, tokens, dim, code, _on(stream, index))
     if status:
         _check(status)
     return q_out, k_out
