@@ -368,3 +368,36 @@ def test_a_fork_after_shortening_into_a_shared_page(w4):
 
 def cache_state_tensors(cache):
     return [cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale]
+
+
+def test_keep_on_pages_past_32_bits(w4):
+    page, pages, lens, counts, paths = 128, 40000, [300, 131], [60, 9], [list(range(5, 60, 3)), [0, 8]]
+    cache = w4.kv8_cache(pages, 8, page, 128)  # 5.2 GB a side
+    small = ref.random_cache(w4, 6, 8, page, 128, seed=50)
+    near = ref.scattered_table(lens, page, 6, seed=51)
+    for big, little in ((cache.k, small.k), (cache.v, small.v)):
+        big.view(torch.uint8)[-6:].copy_(little.view(torch.uint8))
+    cache.k_scale[-6:], cache.v_scale[-6:] = small.k_scale, small.v_scale
+    far = torch.where(near >= 0, near + pages - 6, -1).to(torch.int32)
+    for c, t in ((cache, far), (small, near)):
+        w4.kv8_keep(c, t, ref.ints(lens), ref.bounds(counts), packed(paths, counts), 64)
+    assert w4.w4_device_status() == 0
+    for big, little in zip(cache_state_tensors(cache), cache_state_tensors(small)):
+        assert torch.equal(big[-6:], little) and not (big[:-6] if big.dim() == 4 else big[:-6] - 1).any()
+
+
+def test_many_sequences_are_shortened(w4):
+    seqs = 50000
+    pool = w4.kv8_pool(2 * seqs, seqs, 32, 16)
+    w4.kv8_reserve(pool, torch.full((seqs,), 20, dtype=torch.int32, device="cuda"))
+    drop = torch.arange(seqs, dtype=torch.int32, device="cuda") % 3 * 10
+    w4.kv8_shorten(pool, drop)
+    assert int(pool.status) == 0 and torch.equal(pool.lens, 20 - drop)
+    held = (pool.lens + 15) // 16
+    assert torch.equal((pool.table >= 0).sum(1).int(), held) and int(pool.refs.sum()) == int(held.sum())
+    assert bool((pool.refs[pool.table[pool.table >= 0].long()] == 1).all())
+    drop[seqs - 1] = 21  # one that cannot be: nothing happens to any
+    before = [x.clone() for x in (pool.refs, pool.table, pool.lens)]
+    w4.kv8_shorten(pool, drop)
+    assert int(pool.status) == 14
+    assert all(torch.equal(x, y) for x, y in zip(before, (pool.refs, pool.table, pool.lens)))

@@ -315,3 +315,84 @@ def test_streams(w4):
     torch.cuda.synchronize()
     for pair in got:
         assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_more_sequences_than_a_split_call_takes(w4, tree):
+    """Thousands of sequences, some longer than the window."""
+    batch = 2100
+    rng = np.random.default_rng(55)
+    lens = [int(rng.integers(0, 40)) if b % 50 else 700 + b // 50 for b in range(batch)]
+    counts = [min(2, n) for n in lens]
+    trees = [mask.random_tree(m, rng, "any") for m in counts] if tree else None
+    pages = sum(-(-n // 16) for n in lens)
+    cache = ref.random_cache(w4, pages, 1, 16, 64, seed=56)
+    table = ref.scattered_table(lens, 16, pages, seed=57)
+    q = queries(sum(counts), 3, 64, "bf16", 58)
+    check(w4, q, cache, table, lens, counts, "bf16", 600, 2, trees)
+
+
+@pytest.mark.parametrize("counts,heads", [([1, 1], 4), ([30, 50], 4)])
+def test_pages_past_32_bits(w4, counts, heads):
+    """Codes that lie beyond 2^32 bytes."""
+    lens, page, pages = [900, 333], 128, 40000  # 5.2 GB a side
+    cache = w4.kv8_cache(pages, 8, page, 128)
+    small = ref.random_cache(w4, 12, 8, page, 128, seed=59)
+    near = ref.scattered_table(lens, page, 12, seed=60)
+    for big, little in ((cache.k, small.k), (cache.v, small.v)):
+        big.view(torch.uint8)[-12:].copy_(little.view(torch.uint8))
+    cache.k_scale[-12:], cache.v_scale[-12:] = small.k_scale, small.v_scale
+    far = torch.where(near >= 0, near + pages - 12, -1).to(torch.int32)
+    q = queries(sum(counts), 8 * heads, 128, "fp16", 61)
+    rng = np.random.default_rng(62)
+    words = mask.words_tensor(sum((mask.random_tree(m, rng, "tree") for m in counts), []))
+    for how in (dict(window=200, sinks=5), dict(tree=words), dict(window=100, tree=words)):
+        args = ref.ints(lens), ref.bounds(counts), max(counts), 900
+        assert torch.equal(w4.kv8_attention(q, cache, far, *args, **how), w4.kv8_attention(q, small, near, *args, **how))
+
+
+def test_a_sequence_past_its_bounds(w4):
+    """Longer than max_kv_len or its table row: zeros, and its neighbours are not touched."""
+    lens, counts = [100, 200, 150], [2, 2, 2]
+    cache = ref.random_cache(w4, 30, 2, 16, 64, seed=63)
+    table = ref.scattered_table(lens, 16, 30, seed=64)
+    q = queries(6, 4, 64, "bf16", 65)
+    words = mask.words_tensor([1, 3] * 3)
+    for n, most in (([100, 200, 150], 180), ([100, 16 * table.shape[1] + 1, 150], 1000), ([100, -1, 150], 1000)):
+        for how in (dict(window=50, sinks=1), dict(tree=words)):
+            out = w4.kv8_attention(q, cache, table, ref.ints(n), ref.bounds(counts), 2, most, **how)
+            assert w4.w4_device_status(clear=True) == 14
+            assert not out[2:4].any()
+            rest = [0, 1, 4, 5]
+            sees = lambda b: (mask.window_sees([100, 0, 150][b], 2, 50, 1) if "window" in how  # noqa: E731
+                              else mask.tree_sees([100, 0, 150][b], 2, [1, 3]))
+            want, tol = mask.attention(q, cache, table, [100, 0, 150], counts, sees, 64 ** -0.5, "bf16")
+            assert ((out.double() - want).abs()[rest] <= tol[rest]).all()
+
+
+def test_a_bad_page_counts_as_one_without_tokens(w4):
+    lens, counts = [300], [4]
+    cache = ref.random_cache(w4, 30, 1, 16, 64, seed=66)
+    table = ref.scattered_table(lens, 16, 30, seed=67)
+    q = queries(4, 4, 64, "bf16", 68)
+    args = ref.ints(lens), ref.bounds(counts), 4, 300
+    words = mask.words_tensor(mask.random_tree(4, None, "chain"))
+    for bad in (30, -1, 2 ** 31 - 1, -2 ** 31):
+        for how, spot in ((dict(window=100, sinks=20), 15), (dict(window=100, sinks=20), 1), (dict(tree=words), 7)):
+            broken = table.clone()
+            broken[0, spot] = bad
+            out = w4.kv8_attention(q, cache, broken, *args, **how)
+            assert w4.w4_device_status(clear=True) == 14
+
+            def sees(b):
+                s = mask.window_sees(300, 4, 100, 20) if "window" in how else mask.tree_sees(300, 4, [1, 3, 7, 15])
+                s[:, 16 * spot:16 * spot + 16] = False
+                return s
+
+            want, tol = mask.attention(q, cache, table, lens, counts, sees, 64 ** -0.5, "bf16")
+            assert ((out.double() - want).abs() <= tol).all()
+    # one that no query sees is not looked at
+    broken = table.clone()
+    broken[0, 8] = 30
+    w4.kv8_attention(q, cache, broken, *args, window=100, sinks=20)
+    assert w4.w4_device_status() == 0

@@ -234,3 +234,50 @@ def test_no_tokens(w4):
     x = projection(0, 3, 64, "bf16", 23)
     got = w4.qk_norm_rope(x[:, :2], x[:, 2:], ref.ints([]), w4.rope_table(4, 64), *weights(64, 24))
     assert got[0].shape == (0, 2, 64) and got[1].shape == (0, 1, 64)
+
+
+def test_rows_past_32_bits(w4):
+    """Token rows a megabyte and more apart, offsets beyond 2^32 bytes."""
+    wide = torch.empty((2500, 1 << 20), dtype=torch.bfloat16, device="cuda")
+    src = projection(2500, 3, 128, "bf16", 25)
+    rows = wide[:, :3 * 128].view(2500, 3, 128)
+    rows.copy_(src)
+    table, (wq, wk) = w4.rope_table(2500, 128), weights(128, 26)
+    pos = torch.arange(2500, dtype=torch.int32, device="cuda")
+    want = w4.qk_norm_rope(src[:, :2], src[:, 2:], pos, table, wq, wk)
+    got = w4.qk_norm_rope(rows[:, :2], rows[:, 2:], pos, table, wq, wk, q_out=rows[:, :2], k_out=rows[:, 2:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1024, 1024), (1, 1024), (1024, 3)])
+def test_most_heads(w4, heads, kv_heads):
+    x = projection(3, heads + kv_heads, 64, "fp16", 27)
+    table, (wq, wk), pos = w4.rope_table(9, 64), weights(64, 28), ref.ints([9, 0, 8, 4])[1:]  # 4-byte alignment
+    got = w4.qk_norm_rope(x[:, :heads], x[:, heads:], pos, table, wq, wk)
+    for y, z, w in zip(got, (x[:, :heads], x[:, heads:]), (wq, wk)):
+        check(y, *formula(z, w, pos, table, False))
+
+
+def test_calls_from_several_threads(w4):
+    import threading
+    x, table = projection(50, 6, 128, "bf16", 29), w4.rope_table(100, 128)
+    pos, (wq, wk) = ref.ints(list(range(50))), weights(128, 30)
+    want = w4.qk_norm_rope(x[:, :4], x[:, 4:], pos, table, wq, wk)
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.default_stream())
+        for _ in range(50):
+            got = w4.qk_norm_rope(x[:, :4], x[:, 4:], pos, table, wq, wk, stream=stream)
+            stream.synchronize()
+            if not (torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])):
+                wrong.append(got)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
