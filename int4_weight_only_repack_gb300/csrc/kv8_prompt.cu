@@ -14,13 +14,14 @@
 // warps 8-11 widen them to fp16 (exactly) into the swizzled operand tiles, one
 // layout for K (K-major) and V (MN-major); warp 12 issues the products, tile 0's
 // and tile 1's in turn (issued by a warp each, the tiles fell into step and shared
-// both the tensor cores and the exponentials' units). Registers go where they are
+// both the tensor cores and the exponentials' units); warps 14 and 15 have nothing to
+// do but, in a masked call, to send for a later item's queries. Registers go where they are
 // needed (setmaxnreg 184 / 184 / 96 / 48: four times the 128 of the launch).
 //
 // A masked call's items have the steps of the sinks and those from their first row's
 // window on; which tokens a row sees is a word of 32 bits for each 32 columns, applied
 // where some row of the warp does not see them all. A prompt of 8000 with a window of
-// 1024 (126 GFLOP) takes 189 us: 9.5 steps an item, and 24 000 cycles around them.
+// 1024 (126 GFLOP) takes 185 us: 9.5 steps an item, and 24 000 cycles around them.
 //
 // A CTA takes one item, the longest first (a causal sequence's last tile sees the
 // most). One CTA an SM that walks a list of items, with the next item's codes and
@@ -79,6 +80,7 @@ struct Prompt {
   CUtensorMap tk, tv;  // token rows [pages * heads * page][D] bytes, box of a page
   int tiles;           // of the longest sequence, of CTA_ROWS rows
   int parts;           // of an item
+  int sms;             // of the GPU, where the call is masked
   int bf16, mask;
   float* sums;         // with parts > 1: [item][part][D + 2][CTA_ROWS], sums, maximum, l
 };
@@ -767,6 +769,23 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         if (last >= 0) drain_wait(bars.rawfull(0), last & 1);
         if (last_v >= 0) drain_wait(bars.rawfull(1), last_v & 1);
       }
+    } else if (MASK && !SPLIT && role >= 14) {
+      // ---------------------------------------------------------- a later item's queries, to L2
+      // The item that an SM begins as it ends this one: it has nothing to do until its queries
+      // are there, and an item of a window is short. (Prompt 189 -> 185 us, chunks 210 -> 206;
+      // nothing gained without a mask.)
+      const int later = blockIdx.x + p.sms;
+      if (later < gridDim.x) {
+        const int t = p.tiles - 1 - later / items, bh = later % items, b = bh / a.c.heads, h = bh - b * a.c.heads;
+        const Seq s = load_seq(a, b);
+        for (int k = lane; k < TILE_ROWS; k += 32) {
+          const int row = t * CTA_ROWS + TILE_ROWS * (role - 14) + k, tok = row / a.group;
+          if (row >= s.n * a.group) break;
+          const uint16_t* q = a.q + (size_t)(s.q0 + tok) * a.q_stride + (size_t)(h * a.group + row - tok * a.group) * D;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + c));
+        }
+      }
     }
   }
   tc_fence_before();
@@ -891,6 +910,13 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
   p.a = a;
   p.bf16 = bf16;
   p.mask = mask;
+  p.sms = 0;
+  if (mask) {
+    DeviceInfo info;
+    const cudaError_t e = device_info(&info);
+    if (e != cudaSuccess) return e;
+    p.sms = info.sm_count;
+  }
   p.tiles = (int)(((long long)a.max_q * a.group + CTA_ROWS - 1) / CTA_ROWS);
   // (no more parts than the workspace has room for, which counts all tokens)
   const long long seen = seen_at_most(a, CTA_ROWS / a.group + 2);
