@@ -274,28 +274,32 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     const int tok = (min(rows, first + TILE_ROWS) - 1) / a.group;
     return a.causal && !(MASK && a.tree) ? max(0, min(s.kv, s.kv - s.n + tok + 1)) : s.kv;
   };
-  // a masked item's steps: those of the sinks, and those from its first row's window on
+  // A masked item's steps go through the sinks (whole pages and words of 32 of them) and,
+  // behind them, the pages from its first row's window on: place x there is token at(x).
+  // (Steps of their own for four sinks, and windows that begin with a step, were one step
+  // in ten more.)
   const int first_tok = row0 / a.group, last_tok = (min(rows, row0 + CTA_ROWS) - 1) / a.group;
-  const int sink_steps = MASK ? (int)(((long long)a.sinks + KT - 1) / KT) : 0;
-  const int skip = MASK ? max(0, first_seen(a, s, first_tok) / KT - sink_steps) : 0;
+  const int pages_of = max(32, 1 << a.c.page_shift) - 1;
+  const int sink_end = MASK ? (a.sinks + pages_of) & ~pages_of : 0;
+  const int skip = MASK ? max(0, (first_seen(a, s, first_tok) >> a.c.page_shift << a.c.page_shift) - sink_end) : 0;
+  auto at = [&](int x) { return MASK && x >= sink_end ? x + skip : x; };
   auto steps_of = [&](int tokens) {
-    const int all = (tokens + KT - 1) / KT;
-    return MASK && all > sink_steps ? max(sink_steps, all - skip) : all;
+    const int places = MASK && tokens > sink_end ? max(sink_end, tokens - skip) : tokens;
+    return (places + KT - 1) / KT;
   };
   // this part's: steps0 and steps1 of them from step j0 on
   const int all0 = steps_of(tokens_of(0)), all1 = steps_of(tokens_of(1));
   const int per = (max(all0, all1) + parts - 1) / parts, j0 = part * per, k0 = KT * j0;
   const int steps0 = max(0, min(all0 - j0, per)), steps1 = max(0, min(all1 - j0, per));
   const int steps = max(steps0, steps1);
-  auto token_of = [&](int j) {  // the first of the part's step j
-    if constexpr (MASK) return KT * (j0 + j < sink_steps ? j0 + j : j0 + j + skip);
-    else return k0 + KT * j;
-  };
+  auto place_of = [&](int j) { return k0 + KT * j; };  // the first of the part's step j
   // tokens from which on some row of the CTA does not see all; and, masked, until which
   const int first_lim = a.causal ? max(0, min(s.kv, s.kv - s.n + (MASK && a.tree ? 0 : first_tok + 1))) : s.kv;
   const int all_lo = MASK ? all_see_from(a, s, last_tok) : 0;
-  auto partly_seen = [&](int t) {  // of the step from token t on
-    return t + KT > first_lim || (MASK && t < all_lo && t + KT > a.sinks);
+  auto partly_seen = [&](int x) {  // of the step from place x on
+    if constexpr (!MASK) return x + KT > first_lim;
+    // (a step with sinks and a window begins before all_lo and ends past the sinks)
+    else return at(x + KT - 1) >= first_lim || (at(x) < all_lo && at(x) + KT > a.sinks);
   };
 
   // For the warp that brings codes in: lane g < 8 has the step's sixteen g, its page's
@@ -307,11 +311,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   const bool scales = lane < 8 && (16 * g) % GS == 0;
   const uint32_t page_bytes = (uint32_t)D << shift;
   auto page_at = [&](int j) {
-    const int t = token_of(j) + 16 * g;
+    const int t = at(place_of(j) + 16 * g);
     return j < steps && t < s.kv ? table[t >> shift] : -1;
   };
   auto row_of = [&](int j, int pg) {  // page and head; -1: no page
-    const bool real = j < steps && token_of(j) + 16 * g < s.kv;
+    const bool real = j < steps && at(place_of(j) + 16 * g) < s.kv;
     if (real && (unsigned)pg >= (unsigned)a.c.pages) record(a.status, W4_ERR_PAGE);
     return real && (unsigned)pg < (unsigned)a.c.pages ? pg * a.c.heads + h : -1;
   };
@@ -413,16 +417,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, x[c]);
       const float4* sc = reinterpret_cast<const float4*>(smem + L::OFF_SC) + (j % SLOTS) * SB;
       tmem_ld_wait();
-      const int t0 = token_of(j);
-      if (partly_seen(t0)) {  // some row does not see every token
+      const int x0 = place_of(j);
+      if (partly_seen(x0)) {  // some row does not see every token
         const uint32_t* nan = reinterpret_cast<const uint32_t*>(smem + L::OFF_NAN) + (j % SLOTS) * 4;
-        const int left = sees.lim - t0;
+        const int left = sees.lim - x0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t bad = nan[c];
           if constexpr (MASK) {
             // (a step's mask costs what its exponentials do, so a warp applies what it needs of it)
-            const int t = t0 + 32 * c, d = t - s.kv + s.n;  // d: the draft that the 32 tokens begin with
+            const int t = at(x0 + 32 * c), d = t - s.kv + s.n;  // d: the draft that the 32 tokens begin with
             uint32_t seen = below32(sees.lim - t) & (~below32(sees.lo - t) | below32(a.sinks - t));
             if (d > -32 && d < MAX_DRAFTS) seen |= (uint32_t)(d < 0 ? sees.bits << -d : sees.bits >> d);
             if (bad) {
@@ -613,16 +617,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     // tokens of the step that are none (of a page that does not exist, or past the end)
     auto absent = [&](int j, int slot, int i) {
       const int r = 32 * i + r32;
-      return !(in[slot] >> (r >> 4) & 1) || token_of(j) + r >= s.kv;
+      return !(in[slot] >> (r >> 4) & 1) || at(place_of(j) + r) >= s.kv;
     };
     auto wait_warp = [&](uint32_t bar, uint32_t ph) { return __all_sync(~0u, wait_for(bar, ph, abort_flag, a.status)); };
     for (int j = 0; j < steps; ++j) {
       const int stage = j % KV_STAGES, slot = j % SLOTS;
       const uint32_t ph = ((j / KV_STAGES) & 1) ^ 1;
-      const bool edge = partly_seen(token_of(j));
+      const bool edge = partly_seen(place_of(j));
       if (!wait_warp(bars.rawfull(0), j & 1)) break;
       take(L::OFF_RK);
-      const bool part = token_of(j) + KT > s.kv || in[slot] != 0xFFu;
+      const bool part = at(place_of(j) + KT - 1) >= s.kv || in[slot] != 0xFFu;
       if (part) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
