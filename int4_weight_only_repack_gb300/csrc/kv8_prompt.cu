@@ -21,7 +21,7 @@
 // A masked call's items have the steps of the sinks and those from their first row's
 // window on; which tokens a row sees is a word of 32 bits for each 32 columns, applied
 // where some row of the warp does not see them all. A prompt of 8000 with a window of
-// 1024 (126 GFLOP) takes 185 us: 9.5 steps an item, and 24 000 cycles around them.
+// 1024 (126 GFLOP) takes 179 us: 9 steps an item, and 22 000 cycles around them.
 //
 // A CTA takes one item, the longest first (a causal sequence's last tile sees the
 // most). One CTA an SM that walks a list of items, with the next item's codes and
@@ -31,8 +31,8 @@
 // items as SMs, an item's steps are dealt to several CTAs, whose sums a second
 // kernel joins.
 //
-// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 417 to
-// 422 us, 1250 TFLOP/s, 65 % of the cuBLAS rate. A step takes about 3250 cycles where its
+// Measured: a causal prompt of 8000 tokens, 32 heads on 8 of 128 (524 GFLOP) 415 to
+// 418 us, 1260 TFLOP/s, 66 % of the cuBLAS rate. A step takes about 3250 cycles where its
 // products alone are 2048, and a CTA about 9 us beyond its steps (its first codes
 // and queries, the first step, the output; reading its first page numbers and
 // scales before the barriers are set up is worth 2 to 6 us a call). Neither the
@@ -98,7 +98,7 @@ struct PLayout {
   static constexpr int OFF_NAN = OFF_SC + SLOTS * SB * 16; // [slot][4] tokens with a NaN value
   static constexpr int OFF_IN = OFF_NAN + SLOTS * 16;      // [slot] sixteens that lie in a page
   static constexpr int OFF_BAR = OFF_IN + SLOTS * 4;
-  static constexpr int BARS = 4 * KV_STAGES + 12;
+  static constexpr int BARS = 4 * KV_STAGES + 14;
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;       // + slack to align the base
   static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
@@ -114,6 +114,7 @@ struct PBars {
   __device__ uint32_t pfull(int i) const { return base + 8 * (4 * KV_STAGES + 2 + i); }  // P of tile i
   __device__ uint32_t odone(int i) const { return base + 8 * (4 * KV_STAGES + 4 + i); }  // P V of tile i
   __device__ uint32_t qfull() const { return base + 8 * (4 * KV_STAGES + 6); }
+  __device__ uint32_t qraw(int i) const { return base + 8 * (4 * KV_STAGES + 12 + i); }  // queries as they are
   __device__ uint32_t rawfull(int v) const { return base + 8 * (4 * KV_STAGES + 8 + v); }   // codes of K, V
   __device__ uint32_t rawfree(int v) const { return base + 8 * (4 * KV_STAGES + 10 + v); }
   __device__ uint32_t drained() const { return base + 8 * (4 * KV_STAGES + 7); }  // after a timeout
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       mbar_init(bars.sfull(i), 1);
       mbar_init(bars.pfull(i), SOFT / 64);
       mbar_init(bars.odone(i), 1);
+      mbar_init(bars.qraw(i), TILE_ROWS);
       mbar_init(bars.rawfull(i), 1);
       mbar_init(bars.rawfree(i), CONV / 32);
     }
@@ -368,14 +370,35 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     if constexpr (MASK)
       if (real) sees = sight_of(a, s, tok);
     const int my_steps = i ? steps1 : steps0;
+    bool ok = true;
     float fr;
     {
       const uint16_t* src = a.q + (size_t)(s.q0 + tok) * a.q_stride +
                             (size_t)(h * a.group + (real ? row - tok * a.group : 0)) * D;
       uint4 x[D / 8];
       float amax = 0.f;
+      // A thread that loads its own row touches 32 lines with its warp in each instruction,
+      // and the first codes wait behind them: rows of 256 bytes are copied to their place in
+      // shared memory first, where pieces are taken in turned order, so that the eight lanes
+      // of a phase take them from all banks. (Window of 1024, prompt 184 -> 179 us, chunks
+      // 192 -> 185; no mask, prompt 420 -> 416 us. Rows of 128 bytes lose by it: encoder
+      // states 33.6 -> 35.4 us, chunks with a window 74.0 -> 75.0.)
+      constexpr bool COPY = D == 128;
+      uint8_t* q = smem + i * NB * BLK;
+      if constexpr (COPY) {
+        const uint32_t raw = smem_addr(q) + lrow * (2 * D);
+        mbar_arrive_expect_tx(bars.qraw(i), 2 * D);
+        dec::bulk_copy(raw, src, 2 * D, bars.qraw(i));
+        ok = __all_sync(~0u, wait_for(bars.qraw(i), 0, abort_flag, a.status));
+        if (!ok) drain_wait(bars.qraw(i), 0);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) x[c] = *reinterpret_cast<const uint4*>(src + 8 * c);
+        for (int c = 0; c < D / 8; ++c)
+          x[c] = *reinterpret_cast<const uint4*>(q + lrow * (2 * D) + 16 * ((c + lane) % (D / 8)));
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + i), "n"(TILE_ROWS) : "memory");  // all have taken theirs
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) x[c] = *reinterpret_cast<const uint4*>(src + 8 * c);
+      }
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -387,7 +410,6 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
       const float up = copysignf(e < 128 ? pow2f(14 - e) : 1.f, a.scale_log2);
       fr = fabsf(a.scale_log2) * (e < 128 ? pow2f(e - 14) : 1.f);
-      uint8_t* q = smem + i * NB * BLK;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -395,15 +417,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           y[k] = pack_f16(half_value(w[k] & 0xFFFF, p.bf16) * up, half_value(w[k] >> 16, p.bf16) * up);
-        *reinterpret_cast<uint4*>(q + (c / 8) * BLK + sw(lrow, c % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+        const int pc = COPY ? (c + lane) % (D / 8) : c;
+        *reinterpret_cast<uint4*>(q + (pc / 8) * BLK + sw(lrow, pc % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
     }
     // A row warp sees a step's keys announced before it hands over what the products of
     // that step wait for (Q, then P of the step before): the barrier cannot go on to the
     // step after next, two phases that look alike, while a warp has yet to look.
-    bool ok = true;
-    if (my_steps > 0) ok = __all_sync(~0u, wait_for(bars.kfull(0), 0, abort_flag, a.status));
+    if (ok && my_steps > 0) ok = __all_sync(~0u, wait_for(bars.kfull(0), 0, abort_flag, a.status));
     warp_arrive(bars.qfull());
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t st = tmem + lanes + 128 * i, ot = tmem + lanes + 256 + D * i;
@@ -892,7 +914,7 @@ cudaError_t launch_parts(Prompt& p, cudaStream_t s) {
 
 // Parts of an item: enough to give every SM one, of two steps at least. Measured
 // on one sequence, 8 kv heads and groups of 4, split against not: 128 queries over
-// 32768 tokens 70 against 425 us, 64 over 2048 21 against 37 us; 256 over 1024 were 29
+// 32768 tokens 70 against 425 us, 64 over 2048 20 against 37 us; 256 over 1024 were 29
 // against 25 us when a row's sums were written by its thread (76 and 26 us above):
 // sums in fp32 and a second launch cost some six steps.
 int prompt_parts(long long items, long long max_kv) {
