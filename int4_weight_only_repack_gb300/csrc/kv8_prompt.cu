@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       const uint16_t* src = a.q + (size_t)(s.q0 + tok) * a.q_stride +
                             (size_t)(h * a.group + (real ? row - tok * a.group : 0)) * D;
       uint4 x[D / 8];
-      float amax = 0.f;
+      uint32_t most = 0;  // (magnitudes order as their bits do)
       // A thread that loads its own row touches 32 lines with its warp in each instruction,
       // and the first codes wait behind them: rows of 256 bytes are copied to their place in
       // shared memory first, where pieces are taken in turned order, so that the eight lanes
@@ -403,9 +403,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(half_value(w[k] & 0xFFFF, p.bf16)), fabsf(half_value(w[k] >> 16, p.bf16))));
+        for (int k = 0; k < 4; ++k) most = __vmaxu2(most, w[k] & 0x7FFF7FFFu);
       }
+      const float amax = half_value(max(most & 0xFFFFu, most >> 16), p.bf16);
       // fp16 scaled to [2^14, 2^15); a negative scale goes into Q, so that fr >= 0
       const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
       const float up = copysignf(e < 128 ? pow2f(14 - e) : 1.f, a.scale_log2);
