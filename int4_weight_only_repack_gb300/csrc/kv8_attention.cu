@@ -923,15 +923,24 @@ bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX
 
 // Calls whose windows are short enough for items of their own, however long the
 // sequences are: the windows even out what an item has to read, so it pays longer than
-// ITEM_TOKENS allows, while there are few items. Of their own against split, in us, 4 sinks:
-//   sequences of heads   window 256       600        1000         1500         2000
-//     1 of 32 on 8      6.9 / 11.6   9.6 / 12.7  12.4 / 12.5  15.8 / 12.8  19.3 / 12.4
-//    64 of 64 on 8     15.1 / 17.7  22.3 / 24.4  31.3 / 34.5  41.7 / 45.2  51.1 / 55.2
-//   256 of 32 on 8     59.0 / 39.5  81.0 / 66.9   105 / 97.0   142 / 138    177 / 176
-bool windows_are_short(const Attn& a) {
+// ITEM_TOKENS allows while there are few items, and longest where they fill the CTAs that
+// the GPU holds once. Of their own against split, in us, groups of 8 heads of 128, 4 sinks
+// (sequences of 500 to 20000 tokens, for some of which the window is wide, in brackets):
+//   items   window 1000               2000                        4096
+//      32   12.7 / 12.6               19.8 / 13.9
+//      64   12.9 / 15.2 (13.0 / 15.2) 18.7 / 16.1 (20.0 / 16.0)   34.3 / 19.4 (34.2 / 18.3)
+//     128   13.0 / 16.2 (13.1 / 16.1) 18.8 / 20.0 (20.1 / 20.1)   36.1 / 31.8 (35.1 / 24.0)
+//     192   14.8 / 18.9 (15.1 / 18.9) 22.8 / 23.5 (23.9 / 24.1)   42.1 / 43.8 (42.2 / 33.9)
+//     304   15.2 / 24.1 (15.6 / 23.8) 28.5 / 38.5 (26.7 / 34.8)   51.6 / 61.9 (44.8 / 49.2)
+//     384   27.7 / 28.1 (27.8 / 26.7) 47.6 / 44.6 (41.1 / 41.3)   86.9 / 75.7 (58.3 / 55.9)
+//     608   33.8 / 39.1 (33.3 / 37.8) 54.4 / 61.1 (50.6 / 55.7)   99.7 / 109  (84.9 / 81.7)
+//     768   46.7 / 45.9 (45.8 / 44.7) 73.4 / 75.5 (67.2 / 65.8)    135 / 137  (98.8 / 98.5)
+//    1024   60.8 / 56.5 (55.4 / 54.2) 97.3 / 97.2 (78.0 / 81.2)    178 / 180  ( 121 / 122)
+bool windows_are_short(const Attn& a, int sms) {
   const long long seen = seen_at_most(a, a.max_q);
   const long long items = (long long)a.batch * a.c.heads * (((long long)a.max_q * a.group + 15) / 16);
-  return seen < a.max_kv && seen <= 1024 && items <= 1024;
+  if (seen >= a.max_kv) return false;
+  return (seen <= 1024 && items <= 640) || (seen <= 2112 && items >= 128 && items <= CTAS_PER_SM * sms);
 }
 
 // Rows of queries that share one widening of the codes, in eights.
@@ -1011,7 +1020,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s) {
   const int box = std::min(1 << a.c.page_shift, STEP);
   if (!encode_rows(&r.tk, a.c.k, a.c, a.dim, box) || !encode_rows(&r.tv, a.c.v, a.c, a.dim, box))
     return cudaErrorInvalidValue;
-  r.split = splits(a.batch, a.max_kv) && !windows_are_short(r.a);
+  r.split = splits(a.batch, a.max_kv) && !windows_are_short(r.a, info.sm_count);
   r.bf16 = a.bf16;
   r.rec = static_cast<int*>(a.workspace);
   r.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + MAX_WORKERS * sizeof(Begun));

@@ -396,3 +396,17 @@ def test_a_bad_page_counts_as_one_without_tokens(w4):
     broken[0, 8] = 30
     w4.kv8_attention(q, cache, broken, *args, window=100, sinks=20)
     assert w4.w4_device_status() == 0
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,window,tree", [
+    (20, 16, 8, 1500, False), (20, 16, 8, 1500, True), (40, 8, 8, 2100, False), (33, 4, 2, 900, False)])
+def test_many_windows_of_few_rows(w4, batch, heads, kv_heads, window, tree):
+    """Items that a CTA has whole though they are long, and as many as are split again."""
+    rng = np.random.default_rng(70)
+    lens = [int(rng.integers(3, 4000)) for _ in range(batch)]
+    counts = [int(rng.integers(1, 4)) for _ in range(batch)]
+    trees = [mask.random_tree(m, rng, "tree") for m in counts] if tree else None
+    pages = sum(-(-n // 64) for n in lens)
+    cache = ref.random_cache(w4, pages, kv_heads, 64, 64, seed=71)
+    table = ref.scattered_table(lens, 64, pages, seed=72)
+    check(w4, queries(sum(counts), heads, 64, "fp16", 73), cache, table, lens, counts, "fp16", window, 4, trees)
