@@ -822,13 +822,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   }
 }
 
-// Joins the parts of 32 rows and 32 columns of an item that several CTAs shared: first a
-// warp takes a row, its lanes the parts' maxima and sums of weights; then a lane has a row
-// and a warp four columns, so that reads of the sums are whole lines.
-constexpr int JOIN_ROWS = 32, JOIN_COLS = 32, JOIN_WARPS = 8;
+// Joins the parts of 32 rows and 32 columns of an item that several CTAs shared. A lane has
+// a row and a warp four columns, so that reads of the sums are whole lines, and sixteen
+// parts' are on their way before anything is done with them. The parts' factors come from
+// their maxima and sums of weights: a warp takes a row there, its lanes the parts.
+constexpr int JOIN_ROWS = 32, JOIN_COLS = 32, JOIN_WARPS = 8, JOIN_AHEAD = 16;
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid_constant__ Prompt p) {
-  __shared__ float f_sh[JOIN_ROWS][33], l_sh[JOIN_ROWS];  // a part's factor (-1: it saw nothing), and 1 / l
+  __shared__ float m_sh[32][JOIN_ROWS + 1];                // a part's maximum, then its factor (-1: it saw nothing)
+  __shared__ float w_sh[32][JOIN_ROWS + 1], l_sh[JOIN_ROWS];  // its sum of weights; 1 / l
   __shared__ float o_sh[JOIN_ROWS][JOIN_COLS + 1];
   grid_wait();
   grid_launch_dependents();
@@ -843,38 +845,54 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
   const int row0 = tile * CTA_ROWS + lrow0, rows = min(s.n * a.group - row0, JOIN_ROWS);
   if (rows <= 0 || s.n > a.max_q) return;
   constexpr size_t PITCH = (size_t)CTA_ROWS * (D + 2);
-  const float* from = p.sums + (size_t)item * p.parts * PITCH + lrow0;
-  for (int r = warp; r < rows; r += JOIN_WARPS) {
-    float2 ml = make_float2(NEG_INF, 0.f);  // (at most 32 parts)
-    if (lane < p.parts) {
-      const float* at = from + lane * PITCH + D * CTA_ROWS + r;
-      ml = make_float2(at[0], at[CTA_ROWS]);
+  constexpr int V = JOIN_COLS / JOIN_WARPS;
+  const float* from = p.sums + (size_t)item * p.parts * PITCH + lrow0 + lane;
+  float y[JOIN_AHEAD][V];
+  auto ask = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k) {
+      const bool take = lane < rows && k0 + k < p.parts;
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[k][e] = take ? from[(k0 + k) * PITCH + (size_t)(col0 + V * warp + e) * CTA_ROWS] : 0.f;
     }
-    float top = ml.x;
+  };
+#pragma unroll
+  for (int k = 0; k < 32; k += JOIN_WARPS) {  // (at most 32 parts)
+    float m = NEG_INF, l = 0.f;
+    if (lane < rows && k + warp < p.parts) {
+      const float* at = from + (k + warp) * PITCH + D * CTA_ROWS;
+      m = at[0], l = at[CTA_ROWS];
+    }
+    m_sh[k + warp][lane] = m, w_sh[k + warp][lane] = l;
+  }
+  ask(0);
+  __syncthreads();
+  for (int r = warp; r < rows; r += JOIN_WARPS) {
+    const float m = m_sh[lane][r], w = w_sh[lane][r];
+    float top = m;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     const float base = top == NEG_INF ? 0.f : top;
-    const bool none = ml.x == NEG_INF && ml.y == 0.f;  // (a part that saw only NaN has an l that is not 0)
-    const float f = none ? 0.f : ex2(ml.x - base);
-    float l = none ? 0.f : ml.y * f;
+    const bool none = m == NEG_INF && w == 0.f;  // (a part that saw only NaN has an l that is not 0)
+    const float f = none ? 0.f : ex2(m - base);
+    float l = none ? 0.f : w * f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-    f_sh[r][lane] = none ? -1.f : f;
+    m_sh[lane][r] = none ? -1.f : f;
     if (lane == 0) l_sh[r] = l == 0.f ? 0.f : 1.f / l;
   }
   __syncthreads();
-  constexpr int V = JOIN_COLS / JOIN_WARPS;
   if (lane < rows) {
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < p.parts; ++k) {
-      const float f = f_sh[lane][k];
+    for (int k0 = 0; k0 < p.parts; k0 += JOIN_AHEAD) {
+      if (k0 > 0) ask(k0);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float y = from[k * PITCH + (size_t)(col0 + V * warp + e) * CTA_ROWS + lane];
-        o[e] += f < 0.f ? 0.f : y * f;
+      for (int k = 0; k < JOIN_AHEAD; ++k) {
+        const float f = m_sh[k0 + k][lane];  // (-1 where there is no part)
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] += f < 0.f ? 0.f : y[k][e] * f;
       }
     }
     const float inv = l_sh[lane];
