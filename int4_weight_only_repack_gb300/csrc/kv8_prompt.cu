@@ -822,22 +822,25 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   }
 }
 
-// Joins the parts of 32 rows and 32 columns of an item that several CTAs shared. A lane has
-// a row and a warp four columns, so that reads of the sums are whole lines, and sixteen
-// parts' are on their way before anything is done with them. The parts' factors come from
-// their maxima and sums of weights: a warp takes a row there, its lanes the parts.
-constexpr int JOIN_ROWS = 32, JOIN_COLS = 32, JOIN_WARPS = 8, JOIN_AHEAD = 16;
-template <int D>
+// Joins the parts of 32 rows and some columns of an item that several CTAs shared. A lane
+// has a row and a warp V columns, so that reads of the sums are whole lines, and AHEAD
+// parts' (64 numbers a thread) are on their way before anything is done with them. The
+// parts' factors come from their maxima and sums of weights: a warp takes a row there, its
+// lanes the parts.
+constexpr int JOIN_ROWS = 32, JOIN_WARPS = 8;
+constexpr int join_cols(int d, int ahead) { return std::min(d, 64 / ahead * JOIN_WARPS); }
+template <int D, int AHEAD>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid_constant__ Prompt p) {
+  constexpr int CW = join_cols(D, AHEAD), V = CW / JOIN_WARPS;
   __shared__ float m_sh[32][JOIN_ROWS + 1];                // a part's maximum, then its factor (-1: it saw nothing)
   __shared__ float w_sh[32][JOIN_ROWS + 1], l_sh[JOIN_ROWS];  // its sum of weights; 1 / l
-  __shared__ float o_sh[JOIN_ROWS][JOIN_COLS + 1];
+  __shared__ float o_sh[JOIN_ROWS][CW + 1];
   grid_wait();
   grid_launch_dependents();
   const Attn& a = p.a;
-  constexpr int COLS = D / JOIN_COLS, ROWS = CTA_ROWS / JOIN_ROWS;  // blocks of an item
+  constexpr int COLS = D / CW, ROWS = CTA_ROWS / JOIN_ROWS;  // blocks of an item
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = blockIdx.x % COLS * JOIN_COLS, lrow0 = blockIdx.x / COLS % ROWS * JOIN_ROWS;
+  const int col0 = blockIdx.x % COLS * CW, lrow0 = blockIdx.x / COLS % ROWS * JOIN_ROWS;
   const int item = blockIdx.x / (COLS * ROWS);
   const int items = a.batch * a.c.heads, tile = p.tiles - 1 - item / items, bh = item % items;
   const int b = bh / a.c.heads, h = bh - b * a.c.heads;
@@ -845,12 +848,11 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
   const int row0 = tile * CTA_ROWS + lrow0, rows = min(s.n * a.group - row0, JOIN_ROWS);
   if (rows <= 0 || s.n > a.max_q) return;
   constexpr size_t PITCH = (size_t)CTA_ROWS * (D + 2);
-  constexpr int V = JOIN_COLS / JOIN_WARPS;
   const float* from = p.sums + (size_t)item * p.parts * PITCH + lrow0 + lane;
-  float y[JOIN_AHEAD][V];
+  float y[AHEAD][V];
   auto ask = [&](int k0) {
 #pragma unroll
-    for (int k = 0; k < JOIN_AHEAD; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       const bool take = lane < rows && k0 + k < p.parts;
 #pragma unroll
       for (int e = 0; e < V; ++e) y[k][e] = take ? from[(k0 + k) * PITCH + (size_t)(col0 + V * warp + e) * CTA_ROWS] : 0.f;
@@ -886,10 +888,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-    for (int k0 = 0; k0 < p.parts; k0 += JOIN_AHEAD) {
+    for (int k0 = 0; k0 < p.parts; k0 += AHEAD) {
       if (k0 > 0) ask(k0);
 #pragma unroll
-      for (int k = 0; k < JOIN_AHEAD; ++k) {
+      for (int k = 0; k < AHEAD; ++k) {
         const float f = m_sh[k0 + k][lane];  // (-1 where there is no part)
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] += f < 0.f ? 0.f : y[k][e] * f;
@@ -900,12 +902,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
     for (int e = 0; e < V; ++e) o_sh[lane][V * warp + e] = o[e] * inv;
   }
   __syncthreads();
-  const int r = threadIdx.x / JOIN_WARPS, c = threadIdx.x % JOIN_WARPS * V, row = row0 + r;
+  const int r = threadIdx.x / 8, row = row0 + r;
   if (r >= rows) return;
   const int tok = row / a.group;
-  uint16_t* dst = a.out + ((size_t)(s.q0 + tok) * a.q_heads + h * a.group + (row - tok * a.group)) * D + col0 + c;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half(o_sh[r][c], o_sh[r][c + 1], p.bf16),
-                                              pack_half(o_sh[r][c + 2], o_sh[r][c + 3], p.bf16));
+  uint16_t* dst = a.out + ((size_t)(s.q0 + tok) * a.q_heads + h * a.group + (row - tok * a.group)) * D + col0;
+#pragma unroll
+  for (int c = threadIdx.x % 8 * 4; c < CW; c += 32)
+    *reinterpret_cast<uint2*>(dst + c) = make_uint2(pack_half(o_sh[r][c], o_sh[r][c + 1], p.bf16),
+                                                    pack_half(o_sh[r][c + 2], o_sh[r][c + 3], p.bf16));
 }
 
 template <int D, int GS, bool SPLIT, bool MASK>
@@ -920,8 +924,13 @@ cudaError_t launch_it(Prompt& p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   e = launch(prompt_kernel<D, GS, SPLIT, MASK>, dim3((unsigned)total), THREADS, bytes, s, p);
   if (e != cudaSuccess || !SPLIT) return e;
-  return launch(join_rows_kernel<D>, dim3((unsigned)(items * (CTA_ROWS / JOIN_ROWS) * (D / JOIN_COLS))),
-                32 * JOIN_WARPS, 0, s, p);
+  auto join = [&](auto kernel, int ahead) {
+    return launch(kernel, dim3((unsigned)(items * (CTA_ROWS / JOIN_ROWS) * (D / join_cols(D, ahead)))),
+                  32 * JOIN_WARPS, 0, s, p);
+  };
+  return p.parts <= 4   ? join(join_rows_kernel<D, 4>, 4)
+         : p.parts <= 8 ? join(join_rows_kernel<D, 8>, 8)
+                        : join(join_rows_kernel<D, 16>, 16);
 }
 
 template <int D, int GS>
@@ -939,6 +948,20 @@ int prompt_parts(long long items, long long max_kv) {
   const long long steps = (max_kv + KT - 1) / KT;
   if (steps < SPLIT_STEPS) return 1;
   return (int)std::max<long long>(1, std::min<long long>({SPLIT_SMS / items, steps / 2, 32}));
+}
+
+// Of a masked call, no more than `room`, which the workspace has: none without a step of
+// the longest item (47 steps are 16 parts of 3, not 19); and where a window hides tokens,
+// so that items are short, split only if that leaves out 6 of an item's steps, or 4 where
+// the sums are few. Measured with windows on one sequence of 8000, split against not:
+// groups of 4, 256 queries, a window of 1024 (10 steps, 32 items) 21.3 against 27.3 us,
+// 512 (6 steps) 20.7 against 20.3; 512 queries (64 items in 2 parts), 1536 32.9 against
+// 34.3, 1024 29.4 against 27.7; groups of 1, 128 queries (8 items), 512 15.7 against 19.8.
+int masked_parts(long long items, int room, long long max_kv, long long seen) {
+  const long long steps = (seen + KT - 1) / KT, most = std::max<long long>(1, std::min<long long>(room, steps / 2));
+  const long long per = (steps + most - 1) / most, parts = (steps + per - 1) / per;
+  const bool pays = seen >= max_kv || steps - per >= 6 || (steps - per >= 4 && items * parts <= 64);
+  return pays ? (int)parts : 1;
 }
 
 }  // namespace
@@ -962,13 +985,9 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
     p.sms = info.sm_count;
   }
   p.tiles = (int)(((long long)a.max_q * a.group + CTA_ROWS - 1) / CTA_ROWS);
-  // (no more parts than the workspace has room for, which counts all tokens)
-  const long long seen = seen_at_most(a, CTA_ROWS / a.group + 2);
-  p.parts = prompt_parts((long long)p.tiles * a.c.heads * a.batch, seen);
-  if (mask && p.parts > 1) {  // none without a step of the longest: 47 steps are 16 parts of 3, not 19
-    const long long steps = (seen + KT - 1) / KT, per = (steps + p.parts - 1) / p.parts;
-    p.parts = (int)((steps + per - 1) / per);
-  }
+  const long long items = (long long)p.tiles * a.c.heads * a.batch;
+  p.parts = prompt_parts(items, a.max_kv);
+  if (mask && p.parts > 1) p.parts = masked_parts(items, p.parts, a.max_kv, seen_at_most(a, CTA_ROWS / a.group + 2));
   p.sums = static_cast<float*>(workspace);
   if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, s) : launch_parts<64, 16>(p, s);
   return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, s) : launch_parts<128, 16>(p, s);

@@ -410,3 +410,18 @@ def test_many_windows_of_few_rows(w4, batch, heads, kv_heads, window, tree):
     cache = ref.random_cache(w4, pages, kv_heads, 64, 64, seed=71)
     table = ref.scattered_table(lens, 64, pages, seed=72)
     check(w4, queries(sum(counts), heads, 64, "fp16", 73), cache, table, lens, counts, "fp16", window, 4, trees)
+
+
+@pytest.mark.parametrize("counts,lens,heads,kv_heads,dim,window,sinks,page,tree", [
+    ([70], [3000], 4, 1, 128, 300, 4, 64, False), ([130, 33], [2500, 90], 2, 2, 64, 513, 0, 16, False),
+    ([257], [2100], 4, 4, 128, 900, 40, 32, False), ([200, 300, 1], [2049, 300, 2000], 8, 2, 128, 1100, 1, 64, False),
+    ([60], [5000], 8, 1, 64, 700, 9, 128, True), ([64, 40], [2300, 40], 8, 2, 128, 1500, 0, 64, True),
+    ([150], [2700], 64, 32, 64, 1800, 5, 64, False)])
+def test_prompts_with_short_windows_in_parts(w4, counts, lens, heads, kv_heads, dim, window, sinks, page, tree):
+    """Items of a few steps that several CTAs share, two to eight of them, some without a token."""
+    rng = np.random.default_rng(80)
+    trees = [mask.random_tree(m, rng, "tree") for m in counts] if tree else None
+    pages = sum(-(-n // page) for n in lens)
+    cache = ref.random_cache(w4, pages, kv_heads, page, dim, seed=81)
+    table = ref.scattered_table(lens, page, pages, seed=82)
+    check(w4, queries(sum(counts), heads, dim, "bf16", 83), cache, table, lens, counts, "bf16", window, sinks, trees)
