@@ -81,6 +81,7 @@ struct Prompt {
   int tiles;           // of the longest sequence, of CTA_ROWS rows
   int parts;           // of an item
   int sms;             // of the GPU, where the call is masked
+  int packed;          // blocks for the tiles that sequences have, and no others
   int bf16, mask;
   float* sums;         // with parts > 1: [item][part][D + 2][CTA_ROWS], sums, maximum, l
 };
@@ -237,6 +238,44 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Item x of a call, for a whole warp: false if there is none.
+struct Item {
+  int tile, b, h;
+};
+template <bool PACKED>
+__device__ __forceinline__ bool item_at(const Prompt& p, int x, Item& it) {
+  const Attn& a = p.a;
+  if (!PACKED || !p.packed) {  // the longest rows first: a causal sequence's last tile sees the most
+    const int items = a.batch * a.c.heads, bh = x % items;
+    it.tile = p.tiles - 1 - x / items, it.b = bh / a.c.heads, it.h = bh - it.b * a.c.heads;
+    return true;
+  }
+  int y = x / a.c.heads;
+  it.h = x - y * a.c.heads;
+  auto tiles_in = [&](int b) {  // one at least, which reports a sequence that is left out
+    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0;
+    if (q0 < 0 || n < 0 || q0 > a.total_q - n) return 1;
+    return n > a.max_q ? p.tiles : max(1, (n * a.group + CTA_ROWS - 1) / CTA_ROWS);
+  };
+  const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
+  long long mine = 0;  // (offsets that fall may count rows often)
+#pragma unroll 4
+  for (int b = lane * per; b < min(a.batch, lane * per + per); ++b) mine += tiles_in(b);
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const int owner = __ffs(__ballot_sync(~0u, y < upto)) - 1;
+  if (owner < 0) return false;
+  y -= (int)__shfl_sync(~0u, upto - mine, owner);
+  int t;
+  for (it.b = owner * per; (t = tiles_in(it.b)) <= y; ++it.b) y -= t;
+  it.tile = t - 1 - y;
+  return true;
+}
+
 template <int D, int GS, bool SPLIT, bool MASK>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Prompt p) {
   using L = PLayout<D, GS>;
@@ -253,12 +292,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 
   grid_wait();
   grid_launch_dependents();
-  // the longest rows first: a causal sequence's last tile sees the most
-  const int items = a.batch * a.c.heads;
   const int parts = SPLIT ? p.parts : 1;
   const int item = blockIdx.x / parts, part = blockIdx.x - item * parts;
-  const int tile = p.tiles - 1 - item / items, bh = item % items;
-  const int b = bh / a.c.heads, h = bh - b * a.c.heads;
+  Item it;
+  if (!item_at<MASK && !SPLIT>(p, item, it)) return;
+  const int tile = it.tile, b = it.b, h = it.h;
   const Seq s = load_seq(a, b);
   if (!s.ok && tid == 0 && tile == 0 && part == 0) record(a.status, W4_ERR_PAGE);
   if (s.n > a.max_q) {
@@ -801,9 +839,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       // are there, and an item of a window is short. (Prompt 189 -> 185 us, chunks 210 -> 206;
       // nothing gained without a mask.)
       const int later = blockIdx.x + p.sms;
-      if (later < gridDim.x) {
-        const int t = p.tiles - 1 - later / items, bh = later % items, b = bh / a.c.heads, h = bh - b * a.c.heads;
-        const Seq s = load_seq(a, b);
+      Item to;
+      if (later < gridDim.x && item_at<true>(p, later, to)) {
+        const int t = to.tile, h = to.h;
+        const Seq s = load_seq(a, to.b);
         for (int k = lane; k < TILE_ROWS; k += 32) {
           const int row = t * CTA_ROWS + TILE_ROWS * (role - 14) + k, tok = row / a.group;
           if (row >= s.n * a.group) break;
@@ -912,13 +951,17 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
                                                     pack_half(o_sh[r][c + 2], o_sh[r][c + 3], p.bf16));
 }
 
+// The most tiles that all sequences can have between them: one each is not full.
+long long most_tiles(const Attn& a) { return (long long)a.total_q * a.group / CTA_ROWS + a.batch; }
+
 template <int D, int GS, bool SPLIT, bool MASK>
 cudaError_t launch_it(Prompt& p, cudaStream_t s) {
   static bool done[64] = {};
   constexpr int bytes = PLayout<D, GS>::BYTES;
   cudaError_t e = allow_smem(prompt_kernel<D, GS, SPLIT, MASK>, bytes, done);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.tiles * p.a.c.heads * p.a.batch, total = items * p.parts;
+  const long long items = (p.packed ? most_tiles(p.a) : (long long)p.tiles * p.a.batch) * p.a.c.heads;
+  const long long total = items * p.parts;
   if (total >= (1ll << 30) || !encode_rows(&p.tk, p.a.c.k, p.a.c, D, 1 << p.a.c.page_shift) ||
       !encode_rows(&p.tv, p.a.c.v, p.a.c, D, 1 << p.a.c.page_shift))
     return cudaErrorInvalidValue;
@@ -988,6 +1031,12 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
   const long long items = (long long)p.tiles * a.c.heads * a.batch;
   p.parts = prompt_parts(items, a.max_kv);
   if (mask && p.parts > 1) p.parts = masked_parts(items, p.parts, a.max_kv, seen_at_most(a, CTA_ROWS / a.group + 2));
+  // Sequences of different lengths leave blocks of the longest one's without a row, which
+  // take 0.9 us of an SM each; to find an item by all sequences' lengths takes as long, at
+  // its beginning. So it is found where half of the blocks at least would be without.
+  // (2000 queries beside 63 single ones, 8 kv heads, window of 1024: 235 -> 133 us; 300
+  // beside 15 single ones 48 -> 47; chunks of 100 to 2000, 20 blocks of 32 at most, 182 -> 187.)
+  p.packed = mask && p.parts == 1 && 2 * most_tiles(a) <= (long long)p.tiles * a.batch;
   p.sums = static_cast<float*>(workspace);
   if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, s) : launch_parts<64, 16>(p, s);
   return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, s) : launch_parts<128, 16>(p, s);

@@ -425,3 +425,70 @@ def test_prompts_with_short_windows_in_parts(w4, counts, lens, heads, kv_heads, 
     cache = ref.random_cache(w4, pages, kv_heads, page, dim, seed=81)
     table = ref.scattered_table(lens, page, pages, seed=82)
     check(w4, queries(sum(counts), heads, dim, "bf16", 83), cache, table, lens, counts, "bf16", window, sinks, trees)
+
+
+def mixed(batch, long, rng):
+    """Mostly single tokens, some sequences without one, and few long ones."""
+    counts = [int(rng.integers(0, 3)) for _ in range(batch)]
+    for b, n in long.items():
+        counts[b] = n
+    return counts, [n + int(rng.integers(0, 700)) for n in counts]
+
+
+@pytest.mark.parametrize("batch,long,heads,kv_heads,dim,window,sinks,spare", [
+    (3, {1: 2000}, 2, 2, 128, 100, 4, 0), (40, {0: 600, 39: 257}, 8, 2, 128, 300, 0, 0),
+    (33, {32: 900}, 4, 4, 64, 1000, 33, 7), (65, {2: 513, 40: 512, 64: 1}, 5, 1, 128, 64, 0, 0),
+    (300, {7: 700, 250: 300}, 16, 2, 64, 50, 1, 90)])
+def test_mixed_lengths(w4, batch, long, heads, kv_heads, dim, window, sinks, spare):
+    """Blocks only for the rows that there are, and a graph replayed on other lengths."""
+    rng = np.random.default_rng(90)
+    counts, lens = mixed(batch, long, rng)
+    lens = [max(n, 1) for n in lens]
+    pages = sum(-(-n // 32) for n in lens)
+    cache = ref.random_cache(w4, pages, kv_heads, 32, dim, seed=91)
+    table = ref.scattered_table(lens, 32, pages, seed=92)
+    q = queries(sum(counts) + spare, heads, dim, "bf16", 93).contiguous()
+    check(w4, q, cache, table, lens, counts, "bf16", window, sinks)
+    n, cu = ref.ints(lens), ref.bounds(counts)
+    call = lambda: w4.kv8_attention(q, cache, table, n, cu, max(counts), max(lens), window=window,  # noqa: E731
+                                    sinks=sinks, out=out)
+    out = torch.zeros_like(q)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    turned = counts[::-1] if max(counts[::-1][b] - lens[b] for b in range(batch)) <= 0 else \
+        [min(c, m) for c, m in zip(counts[::-1], lens)]
+    cu.copy_(ref.bounds(turned))
+    out.fill_(float("nan"))
+    graph.replay()
+    sees = lambda b: mask.window_sees(lens[b], turned[b], window, sinks)  # noqa: E731
+    total = sum(turned)
+    want, tol = mask.attention(q[:total], cache, table, lens, turned, sees, dim ** -0.5, "bf16")
+    assert ((out[:total].double() - want).abs() <= tol).all()
+    assert out[total:].isnan().all()
+    assert w4.w4_device_status() == 0
+
+
+def test_mixed_lengths_past_the_bounds(w4):
+    """Too many queries give zeros; offsets that fall leave out their sequence, and those
+    before it are done."""
+    counts, lens = [1, 700, 2, 0, 40, 1] + [1] * 20, [300, 750, 90, 5, 400, 33] + [64] * 20
+    pages = sum(-(-n // 32) for n in lens)
+    cache = ref.random_cache(w4, pages, 2, 32, 128, seed=94)
+    table = ref.scattered_table(lens, 32, pages, seed=95)
+    q = queries(sum(counts), 8, 128, "fp16", 96)
+    sees = lambda b: mask.window_sees(lens[b], counts[b], 90, 2)  # noqa: E731
+    want, tol = mask.attention(q, cache, table, lens, counts, sees, 128 ** -0.5, "fp16")
+    out = w4.kv8_attention(q, cache, table, ref.ints(lens), ref.bounds(counts), 699, 800, window=90, sinks=2)
+    assert w4.w4_device_status(clear=True) == 14
+    assert not out[1:701].any()
+    rest = [0] + list(range(701, sum(counts)))
+    assert ((out.double() - want).abs()[rest] <= tol[rest]).all()
+    cu = ref.bounds(counts)
+    cu[5] = 0  # of sequences 4 and 5: the one falls, the other has the rows of those before it
+    out = torch.zeros_like(q)
+    w4.kv8_attention(q, cache, table, ref.ints(lens), cu, 700, 800, out=out, window=90, sinks=2)
+    assert w4.w4_device_status(clear=True) == 14
+    assert ((out.double() - want).abs()[701:703] <= tol[701:703]).all()
