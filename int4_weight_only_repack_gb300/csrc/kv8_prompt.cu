@@ -21,7 +21,7 @@
 // A masked call's items have the steps of the sinks and those from their first row's
 // window on; which tokens a row sees is a word of 32 bits for each 32 columns, applied
 // where some row of the warp does not see them all. A prompt of 8000 with a window of
-// 1024 (126 GFLOP) takes 179 us: 9 steps an item, and 22 000 cycles around them.
+// 1024 (126 GFLOP) takes 178 us: 9 steps an item, and 22 000 cycles around them.
 //
 // A CTA takes one item, the longest first (a causal sequence's last tile sees the
 // most). One CTA an SM that walks a list of items, with the next item's codes and
@@ -984,9 +984,9 @@ cudaError_t launch_parts(Prompt& p, cudaStream_t s) {
 
 // Parts of an item: enough to give every SM one, of two steps at least. Measured
 // on one sequence, 8 kv heads and groups of 4, split against not: 128 queries over
-// 32768 tokens 70 against 425 us, 64 over 2048 20 against 37 us; 256 over 1024 were 29
-// against 25 us when a row's sums were written by its thread (76 and 26 us above):
-// sums in fp32 and a second launch cost some six steps.
+// 32768 tokens 66 against 425 us, 64 over 2048 18 against 37 us; 256 over 1024 were 29
+// against 25 us when a row's sums were written by its thread and joined one part after
+// another (76 and 26 us above): sums in fp32 and a second launch cost some six steps.
 int prompt_parts(long long items, long long max_kv) {
   const long long steps = (max_kv + KT - 1) / KT;
   if (steps < SPLIT_STEPS) return 1;
