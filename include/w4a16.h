@@ -112,7 +112,9 @@ enum {
     W4_ERR_NO_PAGES = 15,  /* (device) w4_kv8_reserve / _fork: too few free pages       */
     W4_ERR_SEQ = 16,       /* (device) w4_kv8_*: a sequence number was out of range, or a
                               fork's target was not empty or listed twice             */
-    W4_ERR_POSITION = 17   /* (device) w4_qk_norm_rope: a position past the table     */
+    W4_ERR_POSITION = 17,  /* (device) w4_qk_norm_rope: a position past the table     */
+    W4_ERR_SHARED = 18     /* (device) w4_kv8_reserve: a sequence's last page, which would get
+                              new tokens, is another sequence's too                   */
 };
 
 enum { W4_F16 = 0, W4_BF16 = 1 };
@@ -611,15 +613,18 @@ W4_API w4_status w4_kv8_keep(const w4_kv8_cache* cache, const int32_t* table, in
  *
  * w4_kv8_reserve  lens[s] += new_tokens[s] (each >= 0; at most 2^30 tokens then)
  *     for every sequence, and gives it the pages that takes: the lowest free ones,
- *     sequence by sequence. (After an error lens is what it was, and an append that
- *     still follows, in a graph say, takes the last tokens counted there for its own.)
+ *     sequence by sequence. A sequence that would get tokens in a partial last page
+ *     which others hold too is an error (W4_ERR_SHARED): it needs w4_kv8_fork first.
+ *     (After an error lens is what it was, and an append that still follows, in a graph
+ *     say, takes the last tokens counted there for its own.)
  * w4_kv8_shorten  lens[s] -= drop[s] (0 to lens[s]) for every sequence: the pages
  *     beyond its new end lose a reference and leave its table row. A drop or length
  *     out of range, or a bad or free page among those, changes nothing (W4_ERR_PAGE).
  *     (Tables that name a page more often than its references say are found only while
  *     they are changed: such a page stays free, and the call reports W4_ERR_PAGE.)
  *     A last page that other sequences share stays shared: a sequence shortened into it
- *     gets tokens again only after w4_kv8_fork, which copies a last partial page.
+ *     gets tokens again (w4_kv8_reserve refuses it, W4_ERR_SHARED) only after w4_kv8_fork,
+ *     which copies a last partial page, or once the others have let the page go.
  * w4_kv8_fork     for i < n, in order: the empty sequence dst[i] becomes a copy
  *     of src[i], which may be an earlier pair's target. Full pages are shared
  *     (refs + 1); a last partial page is copied into the next free page, which

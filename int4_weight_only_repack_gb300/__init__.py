@@ -828,7 +828,8 @@ def kv8_keep(cache: KV8Cache, table, kv_lens, cu_q, path, max_q_len, stream=None
     (kv_lens counts them): path int32 [tokens], packed like the drafts, lists their
     numbers within the sequence, ascending, then -1. They become the sequence's first
     new tokens, in every layer's cache that this is called for; then shorten the
-    sequences with kv8_shorten. See w4_kv8_keep in include/w4a16.h."""
+    sequences with kv8_shorten. The pages of the drafts must be the sequence's own: fork
+    it before it gets them or after they were kept. See w4_kv8_keep in include/w4a16.h."""
     _one_gpu(cache._device, table, kv_lens, cu_q, path)
     tab, stride, held = _table(table, stream, cache._device)
     status = lib().w4_kv8_keep(cache._ref, tab, stride, _ints(kv_lens, "kv_lens"), _ints(cu_q, "cu_q"),
@@ -881,7 +882,9 @@ def w4_kv8_pages_workspace_size(num_pages, n) -> int:
 
 def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
     """Lengthens every sequence s by new_tokens[s] and gives it the pages that
-    takes, the lowest free ones in order."""
+    takes, the lowest free ones in order. A sequence whose partial last page others
+    hold too (one shortened into what a fork shares, or that fork) is refused, and with
+    it the call (W4_ERR_SHARED): kv8_fork copies such a page."""
     if new_tokens.shape[0] != pool._args[5]:
         raise ValueError("new_tokens must have an entry for every sequence")
     _one_gpu(pool._device, new_tokens)
@@ -895,7 +898,10 @@ def kv8_reserve(pool: KV8Pool, new_tokens, stream=None):
 
 def kv8_shorten(pool: KV8Pool, drop, stream=None):
     """Takes the last drop[s] tokens from every sequence s (rejected drafts, say): the pages
-    beyond its new end lose a reference."""
+    beyond its new end lose a reference. A sequence that now ends within a page that
+    others hold too can be read, forked and shortened; to grow again it has to be forked
+    (kv8_fork and kv8_copy_pages, then kv8_free of the old one), until which kv8_reserve
+    refuses it."""
     if drop.shape[0] != pool._args[5]:
         raise ValueError("drop must have an entry for every sequence")
     _one_gpu(pool._device, drop)

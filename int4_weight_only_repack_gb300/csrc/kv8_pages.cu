@@ -148,10 +148,15 @@ __global__ void __launch_bounds__(BT) __cluster_dims__(CL, 1, 1) reserve_kernel(
   for (int s = lo + lane; s < hi; s += 32) {
     const int held = b.lens[s], add = b.list[s];
     const long long sum = (long long)held + add;
-    if (held < 0 || add < 0 || sum > MAX_KV || sum > ((long long)b.stride << b.shift))
+    if (held < 0 || add < 0 || sum > MAX_KV || sum > ((long long)b.stride << b.shift)) {
       atomicMax(&c.err[0], W4_ERR_PAGE);
-    else
-      need = min(need + pages_of(sum, b.shift) - pages_of(held, b.shift), cap);
+      continue;
+    }
+    need = min(need + pages_of(sum, b.shift) - pages_of(held, b.shift), cap);
+    if (add > 0 && (held & ((1 << b.shift) - 1))) {  // the first new tokens go to a page that it has
+      const int p = b.table[(size_t)s * b.stride + (held >> b.shift)];
+      if (p >= 0 && p < b.pages && b.refs[p] > 1) atomicMax(&c.err[0], W4_ERR_SHARED);
+    }
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) need = min(need + __shfl_xor_sync(~0u, need, d), cap);

@@ -139,6 +139,7 @@ const char* w4_status_string(w4_status s) {
     case W4_ERR_NO_PAGES: return "W4_ERR_NO_PAGES: too few free pages";
     case W4_ERR_SEQ: return "W4_ERR_SEQ: a sequence number is out of range, or a fork's target is not empty";
     case W4_ERR_POSITION: return "W4_ERR_POSITION: a position on the device is past the table";
+    case W4_ERR_SHARED: return "W4_ERR_SHARED: a sequence would get tokens in a page that others hold too; fork it first";
     default: return "unknown w4_status";
   }
 }
