@@ -567,8 +567,9 @@ typedef struct w4_kv8_mask {
  *       bits from n on mean nothing. max_q_len is 64 at most then (else W4_ERR_SHAPE).
  * Codes and scales of tokens that no query of a sequence sees are not read, but for
  * those near the others (within 256 tokens); their pages' numbers may be looked at.
- * The workspace is that of w4_kv8_attention, as is everything else, but that a sequence
- * whose offsets fall may leave out others behind it. A mask with neither
+ * The workspace is that of w4_kv8_attention, as is everything else. (Where offsets fall, a
+ * row that several sequences claim may be any one's of them. Where they leave 0..total_q
+ * or begin past 0 as well, sequences may be left out beside those that do.) A mask with neither
  * window nor tree is W4_ERR_NULL; sinks without a window and causal 0 are W4_ERR_SHAPE.
  */
 W4_API w4_status w4_kv8_attention_masked(const void* q, size_t q_stride, const w4_kv8_cache* cache,

@@ -81,7 +81,6 @@ struct Prompt {
   int tiles;           // of the longest sequence, of CTA_ROWS rows
   int parts;           // of an item
   int sms;             // of the GPU, where the call is masked
-  int packed;          // blocks for the tiles that sequences have, and no others
   int bf16, mask;
   float* sums;         // with parts > 1: [item][part][D + 2][CTA_ROWS], sums, maximum, l
 };
@@ -238,29 +237,57 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Item x of a call, for a whole warp: false if there is none.
+// Item x of a call, for a whole warp: false if there is none. `blocks` is how many its
+// sequence has in each kv head, `from` the first token whose rows are its own (see below).
 struct Item {
-  int tile, b, h;
+  int tile, b, h, from, blocks;
 };
-template <bool PACKED>
-__device__ __forceinline__ bool item_at(const Prompt& p, int x, Item& it) {
+__device__ __forceinline__ bool bad_offsets(const Attn& a, int q0, int n) {
+  return q0 < 0 || n < 0 || q0 > a.total_q - n;
+}
+
+// Item y of a kv head where offsets fall or leave 0..total_q: whoever is behind such a
+// sequence may begin with rows that others before it have, and all rows counted could be
+// many times those that blocks were launched for. So a row is the first sequence's that has
+// it, and a sequence gets blocks for its tiles from its first own row on, one behind the
+// furthest row so far. That is no more than most_tiles(): a sequence with own rows has one
+// block beyond its rows' share, or two where it begins with others' rows, and before each
+// of those lies one that falls and has none.
+__device__ __forceinline__ bool item_among_fallen(const Prompt& p, long long y, Item& it) {
   const Attn& a = p.a;
-  if (!PACKED || !p.packed) {  // the longest rows first: a causal sequence's last tile sees the most
-    const int items = a.batch * a.c.heads, bh = x % items;
-    it.tile = p.tiles - 1 - x / items, it.b = bh / a.c.heads, it.h = bh - it.b * a.c.heads;
-    return true;
-  }
-  int y = x / a.c.heads;
-  it.h = x - y * a.c.heads;
-  auto tiles_in = [&](int b) {  // one at least, which reports a sequence that is left out
-    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0;
-    if (q0 < 0 || n < 0 || q0 > a.total_q - n) return 1;
-    return n > a.max_q ? p.tiles : max(1, (n * a.group + CTA_ROWS - 1) / CTA_ROWS);
-  };
   const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
-  long long mine = 0;  // (offsets that fall may count rows often)
-#pragma unroll 4
-  for (int b = lane * per; b < min(a.batch, lane * per + per); ++b) mine += tiles_in(b);
+  const int b0 = min(a.batch, lane * per), b1 = min(a.batch, b0 + per);
+  if (blockIdx.x == 0 && threadIdx.x == 0) record(a.status, W4_ERR_PAGE);
+  int high = 0;  // behind the rows of this lane's sequences; then of all before them
+  for (int b = b0; b < b1; ++b) {
+    const int q0 = a.cu_q[b], end = a.cu_q[b + 1];
+    if (!bad_offsets(a, q0, end - q0)) high = max(high, end);
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(~0u, high, d);
+    if (lane >= d) high = max(high, o);
+  }
+  high = __shfl_up_sync(~0u, high, 1);
+  if (lane == 0) high = 0;
+  auto blocks_of = [&](int b, int& high) {
+    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0;
+    if (bad_offsets(a, q0, n) || q0 + n <= high) return 0;
+    it.from = max(q0, high) - q0;
+    high = q0 + n;
+    if (n > a.max_q) {  // zeros, by as many blocks as there are, or as it has rows for
+      it.blocks = min(p.tiles, ((n - it.from) * a.group + CTA_ROWS - 1) / CTA_ROWS);
+      it.tile = it.blocks - 1;
+    } else {
+      const int tiles = (n * a.group + CTA_ROWS - 1) / CTA_ROWS;
+      it.blocks = tiles - it.from * a.group / CTA_ROWS;
+      it.tile = tiles - 1;
+    }
+    return it.blocks;
+  };
+  long long mine = 0;
+  int at = high;
+  for (int b = b0; b < b1; ++b) mine += blocks_of(b, at);
   long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -269,14 +296,54 @@ __device__ __forceinline__ bool item_at(const Prompt& p, int x, Item& it) {
   }
   const int owner = __ffs(__ballot_sync(~0u, y < upto)) - 1;
   if (owner < 0) return false;
-  y -= (int)__shfl_sync(~0u, upto - mine, owner);
+  y -= __shfl_sync(~0u, upto - mine, owner);
+  high = __shfl_sync(~0u, high, owner);
+  int t;
+  for (it.b = owner * per; (t = blocks_of(it.b, high)) <= y; ++it.b) y -= t;
+  it.tile -= (int)y;
+  return true;
+}
+
+// LATER: of a block that has another item now; none where offsets fall.
+template <bool PACKED, bool LATER = false>
+__device__ __forceinline__ bool item_at(const Prompt& p, int x, Item& it) {
+  const Attn& a = p.a;
+  it.from = 0, it.blocks = p.tiles;
+  if (!PACKED) {  // the longest rows first: a causal sequence's last tile sees the most
+    const int items = a.batch * a.c.heads, bh = x % items;
+    it.tile = p.tiles - 1 - x / items, it.b = bh / a.c.heads, it.h = bh - it.b * a.c.heads;
+    return true;
+  }
+  int y = x / a.c.heads;
+  it.h = x - y * a.c.heads;
+  bool fallen = false;
+  auto tiles_in = [&](int b) {  // one at least, which reports a sequence that is left out
+    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0;
+    fallen |= bad_offsets(a, q0, n);
+    return n > a.max_q ? p.tiles : max(1, (n * a.group + CTA_ROWS - 1) / CTA_ROWS);
+  };
+  const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
+  int mine = 0;  // (used where no offset falls, so that the rows are total_q at most)
+#pragma unroll 4
+  for (int b = lane * per; b < min(a.batch, lane * per + per); ++b) mine += tiles_in(b);
+  if (__any_sync(~0u, fallen)) return !LATER && item_among_fallen(p, y, it);
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int o = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const int owner = __ffs(__ballot_sync(~0u, y < upto)) - 1;
+  if (owner < 0) return false;
+  y -= __shfl_sync(~0u, upto - mine, owner);
   int t;
   for (it.b = owner * per; (t = tiles_in(it.b)) <= y; ++it.b) y -= t;
   it.tile = t - 1 - y;
   return true;
 }
 
-template <int D, int GS, bool SPLIT, bool MASK>
+// PACKED: masked and unsplit, with blocks for the tiles that the sequences have and no others.
+template <int D, int GS, bool SPLIT, bool MASK, bool PACKED>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Prompt p) {
   using L = PLayout<D, GS>;
   constexpr int NB = L::NB, SB = L::SB;
@@ -289,18 +356,20 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
   const PBars bars{sbase + L::OFF_BAR};
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  int* own_row = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);  // with PACKED: its sequence's first
 
   grid_wait();
   grid_launch_dependents();
   const int parts = SPLIT ? p.parts : 1;
   const int item = blockIdx.x / parts, part = blockIdx.x - item * parts;
   Item it;
-  if (!item_at<MASK && !SPLIT>(p, item, it)) return;
+  if (!item_at<PACKED>(p, item, it)) return;
   const int tile = it.tile, b = it.b, h = it.h;
   const Seq s = load_seq(a, b);
   if (!s.ok && tid == 0 && tile == 0 && part == 0) record(a.status, W4_ERR_PAGE);
   if (s.n > a.max_q) {
-    zero_rows<D>(a, s, h, tile * parts + part, p.tiles * parts);
+    const Seq own = {s.q0 + it.from, s.n - it.from, 0, false};
+    zero_rows<D>(a, own, h, tile * parts + part, it.blocks * parts);
     return;
   }
   const int rows = s.n * a.group, row0 = tile * CTA_ROWS;
@@ -386,6 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     mbar_init(bars.qfull(), SOFT / 32);
     mbar_init(bars.drained(), 1);
     *abort_flag = 0;
+    if (PACKED) *own_row = it.from * a.group;
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -402,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     more_registers<184>();
     const int i = warp >> 2, quarter = warp & 3;
     const int lrow = quarter * 32 + lane, row = row0 + TILE_ROWS * i + lrow;
-    const bool real = row < rows;
+    const bool real = row < rows && (!PACKED || row >= *own_row);
     const int tok = real ? row / a.group : 0;
     Sight sees = {0, !real ? 0 : a.causal ? min(s.kv, s.kv - s.n + tok + 1) : s.kv, 0};
     if constexpr (MASK)
@@ -840,7 +910,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
       // nothing gained without a mask.)
       const int later = blockIdx.x + p.sms;
       Item to;
-      if (later < gridDim.x && item_at<true>(p, later, to)) {
+      if (later < gridDim.x && item_at<PACKED, true>(p, later, to)) {
         const int t = to.tile, h = to.h;
         const Seq s = load_seq(a, to.b);
         for (int k = lane; k < TILE_ROWS; k += 32) {
@@ -954,18 +1024,18 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_rows_kernel(const __grid
 // The most tiles that all sequences can have between them: one each is not full.
 long long most_tiles(const Attn& a) { return (long long)a.total_q * a.group / CTA_ROWS + a.batch; }
 
-template <int D, int GS, bool SPLIT, bool MASK>
+template <int D, int GS, bool SPLIT, bool MASK, bool PACKED = false>
 cudaError_t launch_it(Prompt& p, cudaStream_t s) {
   static bool done[64] = {};
   constexpr int bytes = PLayout<D, GS>::BYTES;
-  cudaError_t e = allow_smem(prompt_kernel<D, GS, SPLIT, MASK>, bytes, done);
+  cudaError_t e = allow_smem(prompt_kernel<D, GS, SPLIT, MASK, PACKED>, bytes, done);
   if (e != cudaSuccess) return e;
-  const long long items = (p.packed ? most_tiles(p.a) : (long long)p.tiles * p.a.batch) * p.a.c.heads;
+  const long long items = (PACKED ? most_tiles(p.a) : (long long)p.tiles * p.a.batch) * p.a.c.heads;
   const long long total = items * p.parts;
   if (total >= (1ll << 30) || !encode_rows(&p.tk, p.a.c.k, p.a.c, D, 1 << p.a.c.page_shift) ||
       !encode_rows(&p.tv, p.a.c.v, p.a.c, D, 1 << p.a.c.page_shift))
     return cudaErrorInvalidValue;
-  e = launch(prompt_kernel<D, GS, SPLIT, MASK>, dim3((unsigned)total), THREADS, bytes, s, p);
+  e = launch(prompt_kernel<D, GS, SPLIT, MASK, PACKED>, dim3((unsigned)total), THREADS, bytes, s, p);
   if (e != cudaSuccess || !SPLIT) return e;
   auto join = [&](auto kernel, int ahead) {
     return launch(kernel, dim3((unsigned)(items * (CTA_ROWS / JOIN_ROWS) * (D / join_cols(D, ahead)))),
@@ -977,7 +1047,8 @@ cudaError_t launch_it(Prompt& p, cudaStream_t s) {
 }
 
 template <int D, int GS>
-cudaError_t launch_parts(Prompt& p, cudaStream_t s) {
+cudaError_t launch_parts(Prompt& p, bool packed, cudaStream_t s) {
+  if (packed) return launch_it<D, GS, false, true, true>(p, s);
   if (p.mask) return p.parts > 1 ? launch_it<D, GS, true, true>(p, s) : launch_it<D, GS, false, true>(p, s);
   return p.parts > 1 ? launch_it<D, GS, true, false>(p, s) : launch_it<D, GS, false, false>(p, s);
 }
@@ -1036,10 +1107,10 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
   // its beginning. So it is found where half of the blocks at least would be without.
   // (2000 queries beside 63 single ones, 8 kv heads, window of 1024: 235 -> 133 us; 300
   // beside 15 single ones 48 -> 47; chunks of 100 to 2000, 20 blocks of 32 at most, 182 -> 187.)
-  p.packed = mask && p.parts == 1 && 2 * most_tiles(a) <= (long long)p.tiles * a.batch;
+  const bool packed = mask && p.parts == 1 && 2 * most_tiles(a) <= (long long)p.tiles * a.batch;
   p.sums = static_cast<float*>(workspace);
-  if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, s) : launch_parts<64, 16>(p, s);
-  return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, s) : launch_parts<128, 16>(p, s);
+  if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, packed, s) : launch_parts<64, 16>(p, packed, s);
+  return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, packed, s) : launch_parts<128, 16>(p, packed, s);
 }
 
 }  // namespace kv8
