@@ -461,7 +461,8 @@ typedef struct w4_norm_rope {
  * and head x:
  *     y = x * (mean(x^2) + eps)^-1/2 * weight        (y = x on a side without weight)
  *     (a, b) -> (a cos - b sin, b cos + a sin)       for the pairs (a, b) of y
- * in fp32 (the squares' sum too: elements up to 2^60), rounded once to dtype.
+ * in fp32 (the squares' sum too: elements up to 2^60, and however small), rounded once to
+ * dtype. With eps 0 a head of zeros is NaN, as the formula has it.
  *   q, k       either may be NULL, for the other side alone. out may be in itself
  *              (the same address and stride); otherwise it overlaps no input. Both
  *              sides may be slices of one projection's rows.

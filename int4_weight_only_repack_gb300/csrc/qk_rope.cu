@@ -25,6 +25,8 @@ namespace {
 
 constexpr int THREADS = 64;  // (blocks of 256 end in steps: 31.4 against 30.0 us on a prompt of 8000)
 
+constexpr float TINY = 0x1p-100f, TINY_UP = 0x1p80f;
+
 struct Side {
   const uint16_t* in;
   uint16_t* out;
@@ -125,8 +127,26 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
       for (int k = 0; k < 8; ++k) sum += a[k] * a[k] + b[k] * b[k];
 #pragma unroll
       for (int d = TEAM / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      float mean = sum * (1.f / D) + r.eps;
+      if constexpr (BF16) {
+        // Squares of elements below 2^-75 leave fp32, which tells where eps is as small (0,
+        // say) and nothing larger stands beside them: such a head is taken 2^80 times.
+        const bool tiny = s.weight && mean < TINY;
+        if (r.eps < TINY && __any_sync(~0u, tiny)) {
+          const float up = tiny ? TINY_UP : 1.f;
+          sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            a[k] *= up, b[k] *= up;
+            sum += a[k] * a[k] + b[k] * b[k];
+          }
+#pragma unroll
+          for (int d = TEAM / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+          if (tiny) mean = sum * (1.f / D) + r.eps * up * up;
+        }
+      }
       if (s.weight) {
-        const float inv = rsqrtf(sum * (1.f / D) + r.eps);
+        const float inv = rsqrtf(mean);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           a[k] *= inv * w[0][k];
