@@ -202,8 +202,11 @@ __device__ __forceinline__ uint16_t* out_row(const Attn& a, const Seg& g, int rr
 }
 
 // SPLIT: every warp has a run of its own; otherwise a CTA has an item. MASK: a window or
-// a tree; what a row sees then stands in shared memory (in registers, as without one, it
-// would spill), its bits for the new tokens and a bound for those before.
+// a tree; what a row sees then stands in shared memory, its bits for the new tokens and a
+// bound for those before: in registers, as without a mask, it would be four numbers for
+// each of a lane's rows, where 255 registers are taken. (With 16 rows and D 128 the split kernels spill even so: 160 bytes
+// stored and 174 loaded, 64 to 72 and 36 to 38 without a mask. No other variant spills.
+// One user's 5 drafts of groups of 8 on 4000 tokens take 20.7 us, 8 of groups of 4 19.5.)
 struct alignas(16) Sees {
   uint64_t drafts;  // bit i: new token i of the sequence
   int lo, pad;
@@ -925,7 +928,8 @@ bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX
 // sequences are: the windows even out what an item has to read, so it pays longer than
 // ITEM_TOKENS allows while there are few items, and longest where they fill the CTAs that
 // the GPU holds once. Of their own against split, in us, groups of 8 heads of 128, 4 sinks
-// (sequences of 500 to 20000 tokens, for some of which the window is wide, in brackets):
+// (sequences of 500 to 20000 tokens, for some of which the window is wide, in brackets;
+// other shapes below):
 //   items   window 1000               2000                        4096
 //      32   12.7 / 12.6               19.8 / 13.9
 //      64   12.9 / 15.2 (13.0 / 15.2) 18.7 / 16.1 (20.0 / 16.0)   34.3 / 19.4 (34.2 / 18.3)
@@ -936,6 +940,19 @@ bool splits(int batch, int max_kv) { return max_kv > ITEM_TOKENS && batch <= MAX
 //     608   33.8 / 39.1 (33.3 / 37.8) 54.4 / 61.1 (50.6 / 55.7)   99.7 / 109  (84.9 / 81.7)
 //     768   46.7 / 45.9 (45.8 / 44.7) 73.4 / 75.5 (67.2 / 65.8)    135 / 137  (98.8 / 98.5)
 //    1024   60.8 / 56.5 (55.4 / 54.2) 97.3 / 97.2 (78.0 / 81.2)    178 / 180  ( 121 / 122)
+// Other shapes, the same way, have the same borders within some per cent, but that past 304
+// items heads of 128 would rather be split at 1000 where the last wave is nearly empty:
+//   groups of 1 of 128     64 13.0 / 14.6 (12.9 / 14.4)   18.7 / 14.9 (19.9 / 15.0)
+//                         304 15.2 / 21.6 (15.6 / 21.5)   28.1 / 35.7 (26.1 / 32.9)
+//                         384 27.1 / 25.3 (27.4 / 24.0)   47.4 / 41.4 (39.9 / 38.2)
+//                         640 43.1 / 37.5 (39.8 / 36.7)   68.9 / 62.3 (53.4 / 54.7)
+//   groups of 4 of 128    304 15.4 / 22.0 (15.8 / 21.9)   28.2 / 36.4 (26.3 / 32.9)
+//                         640 43.5 / 37.9 (40.2 / 37.0)   70.0 / 62.7 (53.8 / 54.3)
+//   groups of 7 of 64      64 11.7 / 13.5 (11.7 / 13.4)   16.8 / 14.2 (18.0 / 14.0)
+//                         304 14.4 / 20.5 (14.5 / 20.3)   21.6 / 28.7 (22.7 / 25.5)
+//                         640 26.1 / 30.6 (26.3 / 29.2)   43.1 / 47.7 (41.4 / 42.0)
+//   groups of 1 of 64     304 14.2 / 18.3 (14.3 / 18.2)   21.6 / 26.1 (22.6 / 24.3)
+//                         640 25.9 / 27.9 (26.4 / 26.7)   42.5 / 45.3 (40.6 / 40.2)
 bool windows_are_short(const Attn& a, int sms) {
   const long long seen = seen_at_most(a, a.max_q);
   const long long items = (long long)a.batch * a.c.heads * (((long long)a.max_q * a.group + 15) / 16);
