@@ -204,9 +204,10 @@ __device__ __forceinline__ uint16_t* out_row(const Attn& a, const Seg& g, int rr
 // SPLIT: every warp has a run of its own; otherwise a CTA has an item. MASK: a window or
 // a tree; what a row sees then stands in shared memory, its bits for the new tokens and a
 // bound for those before: in registers, as without a mask, it would be four numbers for
-// each of a lane's rows, where 255 registers are taken. (With 16 rows and D 128 the split kernels spill even so: 160 bytes
-// stored and 174 loaded, 64 to 72 and 36 to 38 without a mask. No other variant spills.
-// One user's 5 drafts of groups of 8 on 4000 tokens take 20.7 us, 8 of groups of 4 19.5.)
+// each of a lane's rows, where 255 registers are taken. (With 16 rows and D 128 the split
+// kernels spill even so: 160 bytes stored and 174 loaded, 64 to 72 and 36 to 38 without a
+// mask. No other variant spills. One user's 5 drafts of groups of 8 on 4000 tokens take
+// 20.7 us, 8 of groups of 4 19.5.)
 struct alignas(16) Sees {
   uint64_t drafts;  // bit i: new token i of the sequence
   int lo, pad;

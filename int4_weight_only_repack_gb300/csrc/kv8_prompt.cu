@@ -1080,6 +1080,24 @@ int masked_parts(long long items, int room, long long max_kv, long long seen) {
   return pays ? (int)parts : 1;
 }
 
+// Sequences of different lengths leave blocks of the longest one's without a row, which
+// take 0.9 us of an SM each. To find an item by all sequences' lengths takes longer the
+// more there are: some 1 us for 200 of them, and twice that past 768, at each item's
+// beginning. So it is found so where half of the blocks at least would be without a row, and
+// those that an item is spared cost more than it. Found / by number, in us, a chunk beside
+// single tokens: 2000 rows of 4 heads beside 63 of them, 8 kv heads, window of 1024 133 / 235;
+// 300 beside 15 48 / 47; chunks of 100 to 2000, 20 blocks of 32 at most, 187 / 182. Groups
+// of 4 on 2 kv heads of 64, sequences in all, window of 128:
+//   chunk    128          256          512          768         1000         4000
+//     150   15.7 / 18.1  30.9 / 33.1  65.5 / 58.7  92.8 / 85.5   218 / 109   1481 / 571
+//     300   16.2 / 21.9  31.0 / 40.3  65.6 / 73.0  93.2 / 106    218 / 137
+//    2000   20.0 / 67.4  32.1 / 129   68.5 / 247   95.6 / 365    223 / 472   1491 / 2001
+// (16000 of them 21.7 / 2.3 ms beside 150 queries, 21.7 / 8.1 beside 2000.)
+bool packing_pays(const Attn& a, int tiles) {
+  const double blocks = (double)tiles * a.batch, most = (double)most_tiles(a);
+  return 2 * most <= blocks && 0.9 * (blocks / most - 1) >= a.batch * (a.batch > 768 ? 0.01 : 0.005);
+}
+
 }  // namespace
 
 size_t prompt_workspace_bytes(int batch, int max_q, int max_kv, int group, int kv_heads, int dim) {
@@ -1104,12 +1122,7 @@ cudaError_t launch_prompt(const Attn& a, int dim, int bf16, int mask, void* work
   const long long items = (long long)p.tiles * a.c.heads * a.batch;
   p.parts = prompt_parts(items, a.max_kv);
   if (mask && p.parts > 1) p.parts = masked_parts(items, p.parts, a.max_kv, seen_at_most(a, CTA_ROWS / a.group + 2));
-  // Sequences of different lengths leave blocks of the longest one's without a row, which
-  // take 0.9 us of an SM each; to find an item by all sequences' lengths takes as long, at
-  // its beginning. So it is found where half of the blocks at least would be without.
-  // (2000 queries beside 63 single ones, 8 kv heads, window of 1024: 235 -> 133 us; 300
-  // beside 15 single ones 48 -> 47; chunks of 100 to 2000, 20 blocks of 32 at most, 182 -> 187.)
-  const bool packed = mask && p.parts == 1 && 2 * most_tiles(a) <= (long long)p.tiles * a.batch;
+  const bool packed = mask && p.parts == 1 && packing_pays(a, p.tiles);
   p.sums = static_cast<float*>(workspace);
   if (dim == 64) return a.c.page_shift >= 6 ? launch_parts<64, 64>(p, packed, s) : launch_parts<64, 16>(p, packed, s);
   return a.c.page_shift >= 6 ? launch_parts<128, 64>(p, packed, s) : launch_parts<128, 16>(p, packed, s);

@@ -149,3 +149,22 @@ def test_a_graph_replayed_on_offsets_that_fall(w4):
         want, tol, _ = definition(q, cache, table, lens, cu.tolist(), 700, 90, 2, "fp16")
         holds(out, want, tol, slice(None))
         assert w4.w4_device_status(clear=True) == (0 if at is None else 14)
+
+
+@pytest.mark.parametrize("batch,long,heads,kv_heads,dim,window", [
+    (900, 150, 8, 2, 64, 40), (900, 1500, 8, 2, 64, 40), (1500, 2500, 5, 1, 128, 70), (5000, 700, 4, 1, 64, 20)])
+def test_a_chunk_beside_many_sequences(w4, batch, long, heads, kv_heads, dim, window):
+    """Whether blocks are found by the offsets or counted by number, which both happen here."""
+    rng = np.random.default_rng(batch + long)
+    counts = [int(rng.integers(0, 2)) for _ in range(batch)]
+    counts[batch // 3] = long
+    lens = [max(1, c) + int(rng.integers(0, 60)) for c in counts]
+    cu = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    q, cache, table = setting(lens, cu[-1] + 5, heads, kv_heads, dim, "bf16", 16, 140)
+    total = cu[-1]
+    out = torch.full_like(q, float("nan"))
+    w4.kv8_attention(q, cache, table, ref.ints(lens), ref.ints(cu), long, max(lens), out=out, window=window, sinks=3)
+    assert w4.w4_device_status() == 0 and out[total:].isnan().all()
+    sees = lambda b: mask.window_sees(lens[b], counts[b], window, 3)  # noqa: E731
+    want, tol = mask.attention(q[:total], cache, table, lens, counts, sees, dim ** -0.5, "bf16")
+    holds(out, want, tol, slice(0, total))
